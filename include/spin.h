@@ -386,6 +386,158 @@ spin_status_t spin_decode_attention_int4kv_noalloc(const void *q, const uint8_t 
                                                    int32_t out_dtype, spin_stream_t stream);
 
 /*
+ * The INT4 KV cache in pages. A page holds page_size consecutive slots of one sequence for
+ * every kv head, in the layout spin_rope_hadamard_kvquant writes (a contiguous cache
+ * [batch, n_kv_heads, cache_len, ...] is `batch` pages of cache_len slots, so its writer and
+ * the copies below work on either). A sequence's pages are named by its row of a block table
+ * [rows, table_cols] int32: slot j of row b is slot j % page_size of page
+ * table[b][j / page_size]. Table entries behind a row's last page are never used. An entry
+ * outside [0, pages) has no memory behind it: operators that read it see no slot there, and
+ * copies skip it. Page offsets are 64-bit throughout.
+ */
+typedef struct spin_kv_pages_t {
+  uint8_t *k_cache, *v_cache;                /* [pages, n_kv_heads, page_size, head_dim/2], 16-byte aligned */
+  void *k_scale, *k_zero, *v_scale, *v_zero; /* [pages, n_kv_heads, page_size] fp16, 16-byte aligned */
+  int32_t pages, n_kv_heads, page_size, head_dim; /* head_dim 128 */
+} spin_kv_pages_t;
+
+/*
+ * Attention of each sequence's newest tokens over the INT4 KV cache in pages: one token per
+ * sequence (a decode step), several (drafted tokens, verified together) or a chunk of a
+ * prompt, ragged over the batch ("SpinQuant Guide: Learned Rotations for 4-Bit LLMs", the KV4
+ * serving diagram). The tokens' own keys and values are in the cache already. Token i of the
+ * nq = cu_q[b+1] - cu_q[b] of sequence b stands at position p = lens[b] - nq + i and sees the
+ * slots j <= p with, if window > 0, also (j > p - window or j < sinks). For query head h and
+ * its kv head g = h / (n_q_heads / n_kv_heads):
+ *   khat_j = (code_j - zero_j) * scale_j      (K and V alike, fp16 scale and zero)
+ *   out_h = sum_j softmax_j(softmax_scale * (q_h . khat_j)) * vhat_j   over the visible slots
+ * A token that sees no slot (a position below 0, lens[b] <= 0) gives 0. Products are exact,
+ * weights carry 16 bits, sums are fp32; the same call gives the same bits.
+ *
+ *  q            [tokens, n_q_heads, head_dim] bf16 (rotated queries), 16-byte aligned
+ *  cache        pages as above; page_size a power of two, 16 .. 65536
+ *  block_table  [seqs, table_cols] int32
+ *  lens         [seqs] int32, slots of each sequence, the new tokens' among them; a value
+ *               outside [0, table_cols * page_size] is clamped to it
+ *  cu_q         [seqs + 1] int32, token offsets (ascending, within [0, tokens], clamped to it);
+ *               NULL: one token per sequence, tokens == seqs. Rows of out outside
+ *               [cu_q[0], cu_q[seqs]) are left as they were.
+ *  max_q_len    the largest nq expected (>= 1): chooses the kernel and sizes the workspace;
+ *               larger nq are computed all the same
+ *  n_q_heads    a multiple of cache->n_kv_heads; tokens * n_q_heads < 2^31
+ *  softmax_scale  > 0 and finite, usually 1 / sqrt(head_dim)
+ *  window       >= 0, 0 for none; sinks >= 0 (without a window they change nothing)
+ *  out          [tokens, n_q_heads, head_dim] bf16 or fp32 (out_dtype), 16-byte aligned
+ *  workspace    caller-owned device scratch of at least
+ *               spin_paged_attention_workspace_bytes(n_q_heads, n_kv_heads, max_q_len) bytes,
+ *               16-byte aligned, contents on entry do not matter; calls (and captured graphs)
+ *               that may run at the same time need separate workspaces
+ * block_table, lens and cu_q are read on the device: a captured graph may be replayed after
+ * their contents (not their sizes) change. seqs == 0 or tokens == 0 is a no-op.
+ * Errors: SPIN_ERR_INVALID_ARG (null pointer, negative size, tokens != seqs without cu_q,
+ * softmax_scale, out_dtype, workspace too small), SPIN_ERR_UNSUPPORTED_SIZE (head_dim,
+ * page_size, head counts, tokens), SPIN_ERR_MISALIGNED, SPIN_ERR_DEVICE, SPIN_ERR_CUDA.
+ */
+spin_status_t spin_paged_attention_int4kv(const void *q, int32_t tokens, const spin_kv_pages_t *cache,
+                                          const int32_t *block_table, int32_t seqs, int32_t table_cols,
+                                          const int32_t *lens, const int32_t *cu_q, int32_t max_q_len,
+                                          int32_t n_q_heads, float softmax_scale, int32_t window, int32_t sinks,
+                                          void *out, int32_t out_dtype, void *workspace, size_t workspace_bytes,
+                                          spin_stream_t stream);
+
+/* Workspace bytes spin_paged_attention_int4kv needs: two pieces of a row tile per thread
+ * block, whatever the lengths; 0 for sizes <= 0 or n_q_heads % n_kv_heads != 0. */
+size_t spin_paged_attention_workspace_bytes(int32_t n_q_heads, int32_t n_kv_heads, int32_t max_q_len);
+
+/*
+ * Copy whole pages: page dst_pages[i] of `dst` <- page src_pages[i] of `src`, codes, scales and
+ * zeros, for i < n. `src` and `dst` may be the same cache; they agree in n_kv_heads, page_size
+ * and head_dim. A pair with an id outside its cache is skipped. A page may be the source of
+ * several pairs; a page that is the destination of two pairs, or source and destination in one
+ * call, ends with unspecified contents (no other page is affected).
+ *  src_pages, dst_pages  [n] int32 in device memory; n >= 0 (0 is a no-op)
+ * Errors: SPIN_ERR_INVALID_ARG, SPIN_ERR_UNSUPPORTED_SIZE (head_dim, geometries that differ),
+ * SPIN_ERR_MISALIGNED, SPIN_ERR_DEVICE, SPIN_ERR_CUDA.
+ */
+spin_status_t spin_kv_pages_copy(const spin_kv_pages_t *src, const int32_t *src_pages, const spin_kv_pages_t *dst,
+                                 const int32_t *dst_pages, int32_t n, spin_stream_t stream);
+
+/*
+ * Copy slots: for every row b and cu_keep[b] <= e < cu_keep[b + 1], slot keep[e] of source row b
+ * goes to slot dst_start[b] + e - cu_keep[b] of destination row b (all kv heads, codes, scales
+ * and zeros). It compacts (keep the slots an eviction policy or an accepted draft left), gathers
+ * into another page size, and appends: the slots spin_rope_hadamard_kvquant wrote to a small
+ * contiguous cache (its rows are pages of cache_len slots) move to the pages of ragged
+ * sequences. Entries with a negative slot, a slot outside the row or without a page on either
+ * side are skipped. Destination slots must not be source slots of the same call, nor named
+ * twice; such slots end with unspecified contents.
+ *  src_table  [rows, src_cols] int32, dst_table [rows, dst_cols] int32
+ *  keep       [n] int32; cu_keep [rows + 1] int32 ascending; entries of keep outside
+ *             [cu_keep[0], cu_keep[rows]) are not used
+ *  dst_start  [rows] int32 or NULL (0)
+ *  src, dst agree in n_kv_heads and head_dim; page sizes are free
+ * Errors: as spin_kv_pages_copy.
+ */
+spin_status_t spin_kv_slots_copy(const spin_kv_pages_t *src, const int32_t *src_table, int32_t src_cols,
+                                 const int32_t *keep, const int32_t *cu_keep, int32_t n, int32_t rows,
+                                 const spin_kv_pages_t *dst, const int32_t *dst_table, int32_t dst_cols,
+                                 const int32_t *dst_start, spin_stream_t stream);
+
+/*
+ * The page pool's bookkeeping, in device memory beside the cache: how many rows hold each page,
+ * and a stack of the pages nobody holds (the top is free_pages[*free_count - 1]). The three
+ * calls below change it on `stream`; calls on one pool must be ordered (one stream, or events).
+ * Rows and pages are taken in a fixed order, so the results repeat. A row that cannot be served
+ * is left as it was and says so in `status`: nothing is half done.
+ */
+typedef struct spin_kv_pool_t {
+  int32_t *refs;       /* [pages] rows that hold the page, 0 for a free one */
+  int32_t *free_pages; /* [pages] stack */
+  int32_t *free_count; /* [1] */
+} spin_kv_pool_t;
+
+/* Values of `status`, per row or fork. */
+#define SPIN_KV_OK 0       /* done */
+#define SPIN_KV_NO_PAGES 1 /* not enough free pages */
+#define SPIN_KV_REFUSED 2  /* a bad index, length or count, a child that is not empty, no column left */
+
+/*
+ * Make room for add[b] more slots in every row b: pages are popped for the slots that no page
+ * of the row holds yet (refs 1), their ids written to the row's next columns, and lens[b] grows
+ * by add[b]. Rows are served in order: row b gets its pages if the pages wanted by rows 0 .. b
+ * together are free (refused rows want none); a row that wants none is always served. The last
+ * page of a row that is partly filled is assumed to be the row's own, as after
+ * spin_kv_pages_fork: cut a forked row no shorter than it was when forked.
+ *  block_table [rows, table_cols], lens [rows], add [rows], status [rows]: int32
+ */
+spin_status_t spin_kv_pages_reserve(const spin_kv_pages_t *cache, const spin_kv_pool_t *pool, int32_t *block_table,
+                                    int32_t rows, int32_t table_cols, int32_t *lens, const int32_t *add,
+                                    int32_t *status, spin_stream_t stream);
+
+/*
+ * Fork sequences: row children[i] becomes a second holder of row parents[i]'s full pages
+ * (refs + 1) and gets the filled slots of its last, partly filled page in a page of its own,
+ * popped from the stack and copied, so that both rows can be written on; its other columns
+ * become -1, its length is the parent's. All parents are read as they were before the call. The child row must be empty
+ * (length 0); of several forks into one row the first counts. Forks are served in order, as rows
+ * in spin_kv_pages_reserve.
+ *  parents, children, status  [n] int32; block_table [rows, table_cols]; lens [rows]
+ */
+spin_status_t spin_kv_pages_fork(const spin_kv_pages_t *cache, const spin_kv_pool_t *pool, int32_t *block_table,
+                                 int32_t rows, int32_t table_cols, int32_t *lens, const int32_t *parents,
+                                 const int32_t *children, int32_t n, int32_t *status, spin_stream_t stream);
+
+/*
+ * Let rows go: each listed row gives up its pages (refs - 1), its columns become -1 and its
+ * length 0; pages that nobody holds any more go on the free stack in ascending
+ * order. A row that is empty, listed twice or outside [0, rows) gives up nothing (more).
+ *  list  [n] int32
+ */
+spin_status_t spin_kv_pages_free(const spin_kv_pages_t *cache, const spin_kv_pool_t *pool, int32_t *block_table,
+                                 int32_t rows, int32_t table_cols, int32_t *lens, const int32_t *list, int32_t n,
+                                 spin_stream_t stream);
+
+/*
  * Device status word of the current device: nonzero once a kernel of this
  * library gave up on an internal wait (a pipeline barrier that did not
  * complete within about two seconds); that kernel then stopped early and its

@@ -22,6 +22,8 @@ __all__ = [
     "hadamard_quant_host", "hadamard_quant_kron", "decode_attention_int4kv", "decode_attention_workspace_bytes",
     "rope_hadamard_kvquant",
     "dequant_hadamard_inverse", "alloc_kv_cache", "NO_ROTATE", "SYM_INT4_F32SCALE", "ASYM_INT4_F16SZ",
+    "paged_attention_int4kv", "paged_attention_workspace_bytes", "alloc_kv_pages", "copy_kv_pages", "copy_kv_slots",
+    "reserve_kv_pages", "fork_kv_pages", "free_kv_pages", "KV_OK", "KV_NO_PAGES", "KV_REFUSED",
     "BF16", "F32", "HEADER", "LIB_PATH", "exported_symbols", "CUDA_CORES_ONLY", "TENSOR_CORES", "device_status",
 ]
 
@@ -36,9 +38,23 @@ SYM_INT4_F32SCALE = 0
 ASYM_INT4_F16SZ = 1
 BF16 = 0
 F32 = 1
+KV_OK = 0
+KV_NO_PAGES = 1
+KV_REFUSED = 2
 
 _STATUS = {0: "SPIN_OK", 1: "SPIN_ERR_INVALID_ARG", 2: "SPIN_ERR_UNSUPPORTED_SIZE",
            3: "SPIN_ERR_MISALIGNED", 4: "SPIN_ERR_CUDA", 5: "SPIN_ERR_DEVICE"}
+
+
+class _KvPages(C.Structure):
+    """spin_kv_pages_t"""
+    _fields_ = [(n, C.c_void_p) for n in ("k_cache", "v_cache", "k_scale", "k_zero", "v_scale", "v_zero")] + \
+        [(n, C.c_int32) for n in ("pages", "n_kv_heads", "page_size", "head_dim")]
+
+
+class _KvPool(C.Structure):
+    """spin_kv_pool_t"""
+    _fields_ = [(n, C.c_void_p) for n in ("refs", "free_pages", "free_count")]
 
 
 class SpinError(RuntimeError):
@@ -76,6 +92,19 @@ def lib() -> C.CDLL:
     L.spin_w4a4_gemm.argtypes = [vp, vp, i64, vp, vp, i32, i32, vp, i32, vp]
     L.spin_decode_attention_workspace_bytes.argtypes = [i32, i32, i32]
     L.spin_decode_attention_workspace_bytes.restype = C.c_size_t
+    kv, pool = C.POINTER(_KvPages), C.POINTER(_KvPool)
+    L.spin_paged_attention_int4kv.argtypes = [vp, i32, kv, vp, i32, i32, vp, vp, i32, i32, f32, i32, i32, vp, i32, vp,
+                                              C.c_size_t, vp]
+    L.spin_paged_attention_workspace_bytes.argtypes = [i32, i32, i32]
+    L.spin_paged_attention_workspace_bytes.restype = C.c_size_t
+    L.spin_kv_pages_copy.argtypes = [kv, vp, kv, vp, i32, vp]
+    L.spin_kv_slots_copy.argtypes = [kv, vp, i32, vp, vp, i32, i32, kv, vp, i32, vp, vp]
+    L.spin_kv_pages_reserve.argtypes = [kv, pool, vp, i32, i32, vp, vp, vp, vp]
+    L.spin_kv_pages_fork.argtypes = [kv, pool, vp, i32, i32, vp, vp, vp, i32, vp, vp]
+    L.spin_kv_pages_free.argtypes = [kv, pool, vp, i32, i32, vp, vp, i32, vp]
+    for name in ("spin_paged_attention_int4kv", "spin_kv_pages_copy", "spin_kv_slots_copy", "spin_kv_pages_reserve",
+                 "spin_kv_pages_fork", "spin_kv_pages_free"):
+        getattr(L, name).restype = C.c_int
     for name in ("spin_hadamard_quant_int4", "spin_hadamard_quant_int4_ex", "spin_hadamard_quant_int8",
                  "spin_rope_hadamard_kvquant", "spin_dequant_hadamard_inverse", "spin_hadamard_quant_kron",
                  "spin_decode_attention_int4kv", "spin_w4a4_gemm"):
@@ -438,6 +467,233 @@ def decode_attention_int4kv(q: torch.Tensor, cache: dict, lens: torch.Tensor, so
         F32 if out.dtype == torch.float32 else BF16, _ptr(workspace), workspace.numel(), _stream(stream))
     _check("spin_decode_attention_int4kv", st)
     return out
+
+
+# ------------------------------------------------------------------ the INT4 KV cache in pages
+_KV_CODES = ("k_cache", "v_cache")
+_KV_STEPS = ("k_scale", "k_zero", "v_scale", "v_zero")
+
+
+def _device_of(t: torch.Tensor, stream):
+    """The stream a call runs on, with its device made current if it is not: (stream handle,
+    device to go back to or None)."""
+    if stream is None:
+        stream = torch.cuda.current_stream(t.device)
+    now = torch.cuda.current_device()
+    if t.device.index != now:
+        torch.cuda.set_device(t.device)
+        return stream.cuda_stream, now
+    return stream.cuda_stream, None
+
+
+def _call(fn: str, t: torch.Tensor, stream, *args) -> None:
+    """Run a library entry point on `t`'s device and its current (or the given) stream."""
+    handle, back = _device_of(t, stream)
+    try:
+        _check(fn, getattr(lib(), fn)(*args, handle))
+    finally:
+        if back is not None:
+            torch.cuda.set_device(back)
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A tensor the call on `stream` writes: the caching allocator orders a block's reuse on the
+    stream it was made on, so it is made on that one."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _ints(t: torch.Tensor, name: str, device, shape) -> None:
+    """A contiguous int32 CUDA tensor of the given shape (-1: any size) on the cache's device."""
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name}: expected torch.int32, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.dim() != len(shape) or any(n not in (-1, m) for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _pages(cache: dict, what: str = "cache") -> _KvPages:
+    """Check a cache dict ([pages, n_kv_heads, page_size, d/2] codes, [pages, n_kv_heads,
+    page_size] fp16 scales and zeros) and describe it for the library."""
+    k = cache["k_cache"]
+    if k.dim() != 4:
+        raise ValueError(f"{what}: k_cache is [pages, n_kv_heads, page_size, head_dim / 2], got {tuple(k.shape)}")
+    device, shape = k.device, k.shape
+    if not k.is_cuda:
+        raise ValueError(f"{what}: k_cache must be a CUDA tensor")
+    ptrs = []
+    for names, dtype, want in ((_KV_CODES, torch.uint8, shape), (_KV_STEPS, torch.float16, shape[:3])):
+        for name in names:
+            t = cache[name]
+            if t.dtype != dtype:
+                raise TypeError(f"{what}: {name}: expected {dtype}, got {t.dtype}")
+            if t.device != device or t.shape != want or not t.is_contiguous():
+                raise ValueError(f"{what}: {name} must be a contiguous {tuple(want)} tensor on {device}")
+            ptrs.append(t.data_ptr())
+    return _KvPages(*ptrs, shape[0], shape[1], shape[2], 2 * shape[3])
+
+
+def _pool(pool: dict, block_table: torch.Tensor, lens: torch.Tensor):
+    kv = _pages(pool, "pool")
+    device, pages = pool["k_cache"].device, pool["k_cache"].shape[0]
+    for name, n in (("refs", pages), ("free_pages", pages), ("free_count", 1)):
+        _ints(pool[name], name, device, (n,))
+    _ints(block_table, "block_table", device, (-1, -1))
+    _ints(lens, "lens", device, (block_table.shape[0],))
+    return kv, _KvPool(pool["refs"].data_ptr(), pool["free_pages"].data_ptr(), pool["free_count"].data_ptr()), device
+
+
+def alloc_kv_pages(pages: int, n_kv_heads: int, page_size: int = 64, head_dim: int = 128, device="cuda") -> dict:
+    """A pool of empty pages: the cache arrays of alloc_kv_cache(pages, n_kv_heads, page_size)
+    and the bookkeeping reserve_kv_pages, fork_kv_pages and free_kv_pages keep beside them
+    (refs, free_pages, free_count). Page 0 is handed out first."""
+    pool = alloc_kv_cache(pages, n_kv_heads, page_size, head_dim, device)
+    pool["refs"] = torch.zeros((pages,), dtype=torch.int32, device=device)
+    pool["free_pages"] = torch.arange(pages - 1, -1, -1, dtype=torch.int32, device=device)
+    pool["free_count"] = torch.full((1,), pages, dtype=torch.int32, device=device)
+    return pool
+
+
+def paged_attention_workspace_bytes(n_q_heads: int, n_kv_heads: int, max_q_len: int = 1) -> int:
+    """Scratch bytes paged_attention_int4kv needs (see spin_paged_attention_workspace_bytes)."""
+    return int(lib().spin_paged_attention_workspace_bytes(int(n_q_heads), int(n_kv_heads), int(max_q_len)))
+
+
+def paged_attention_int4kv(q: torch.Tensor, cache: dict, block_table: torch.Tensor, lens: torch.Tensor,
+                           cu_q: torch.Tensor | None = None, max_q_len: int = 1, softmax_scale: float | None = None,
+                           window: int = 0, sinks: int = 0, out_dtype=torch.float32, out: torch.Tensor | None = None,
+                           workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of each sequence's newest tokens over the INT4 KV cache in pages: q [tokens, hq,
+    d] bf16 (rotated queries), cache of pages ([pages, hkv, page_size, d/2] codes), block_table
+    [seqs, cols] int32, lens [seqs] int32 slots of each sequence (the new tokens' among them),
+    cu_q [seqs + 1] int32 token offsets (None: one token per sequence), max_q_len the most tokens
+    a sequence has. Token i of nq sees slots j <= p = lens - nq + i, with a window only those
+    with j > p - window or j < sinks. Returns out [tokens, hq, d] (fp32 or bf16); rows of a given
+    `out` behind the last sequence are left as they were. `workspace` (uint8, at least
+    paged_attention_workspace_bytes) is allocated through torch when not given."""
+    kv = _pages(cache)
+    if q.dim() != 3:
+        raise ValueError(f"q: expected [tokens, n_q_heads, head_dim], got shape {tuple(q.shape)}")
+    tokens, hq, d = q.shape
+    device = cache["k_cache"].device
+    _need(q, "q", torch.bfloat16, device, (tokens, hq, kv.head_dim))
+    _ints(block_table, "block_table", device, (-1, -1))
+    seqs, cols = block_table.shape
+    _ints(lens, "lens", device, (seqs,))
+    if cu_q is not None:
+        _ints(cu_q, "cu_q", device, (seqs + 1,))
+    elif tokens != seqs:
+        raise ValueError(f"{tokens} tokens for {seqs} sequences need cu_q")
+    if out is None:
+        if out_dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"out_dtype: expected torch.float32 or torch.bfloat16, got {out_dtype}")
+        out = _empty((tokens, hq, d), out_dtype, device, stream)
+    else:
+        if out.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"out: expected torch.float32 or torch.bfloat16, got {out.dtype}")
+        _need(out, "out", out.dtype, device, (tokens, hq, d))
+    if workspace is None:
+        need = lib().spin_paged_attention_workspace_bytes(hq, kv.n_kv_heads, max_q_len)
+        workspace = _empty((max(need, 16),), torch.uint8, device, stream)
+    else:
+        _need(workspace, "workspace", torch.uint8, device)
+    scale = float(softmax_scale) if softmax_scale is not None else 1.0 / float(d) ** 0.5
+    _call("spin_paged_attention_int4kv", q, stream, q.data_ptr(), tokens, kv, block_table.data_ptr(), seqs, cols,
+          lens.data_ptr(), _ptr(cu_q), max_q_len, hq, scale, window, sinks, out.data_ptr(),
+          F32 if out.dtype == torch.float32 else BF16, workspace.data_ptr(), workspace.numel())
+    return out
+
+
+def copy_kv_pages(src: dict, src_pages: torch.Tensor, dst_pages: torch.Tensor, dst: dict | None = None,
+                  stream=None) -> dict:
+    """Page dst_pages[i] of `dst` (default: `src` itself) <- page src_pages[i] of `src`, codes,
+    scales and zeros; int32 [n] ids, pairs with an id out of range are skipped. No page may be
+    source and destination, or destination twice, in one call. Returns dst."""
+    dst = src if dst is None else dst
+    a, b = _pages(src, "src"), _pages(dst, "dst")
+    device = src["k_cache"].device
+    if dst["k_cache"].device != device:
+        raise ValueError(f"dst must be on {device}")
+    _ints(src_pages, "src_pages", device, (-1,))
+    _ints(dst_pages, "dst_pages", device, (src_pages.shape[0],))
+    _call("spin_kv_pages_copy", src_pages, stream, a, src_pages.data_ptr(), b, dst_pages.data_ptr(),
+          src_pages.shape[0])
+    return dst
+
+
+def copy_kv_slots(src: dict, src_table: torch.Tensor, keep: torch.Tensor, cu_keep: torch.Tensor, dst: dict,
+                  dst_table: torch.Tensor, dst_start: torch.Tensor | None = None, stream=None) -> dict:
+    """Slot keep[e] of source row b -> slot dst_start[b] + e - cu_keep[b] of destination row b,
+    for cu_keep[b] <= e < cu_keep[b + 1], all heads: compaction, gathering into another page
+    size, or appending the slots of a small contiguous cache (its own table is one page per row:
+    torch.arange(rows)[:, None]). Tables [rows, cols], keep [n], cu_keep [rows + 1], dst_start
+    [rows] (None: 0), all int32. Destination slots must not be source slots. Returns dst."""
+    a, b = _pages(src, "src"), _pages(dst, "dst")
+    device = src["k_cache"].device
+    if dst["k_cache"].device != device:
+        raise ValueError(f"dst must be on {device}")
+    _ints(src_table, "src_table", device, (-1, -1))
+    rows = src_table.shape[0]
+    _ints(dst_table, "dst_table", device, (rows, -1))
+    _ints(keep, "keep", device, (-1,))
+    _ints(cu_keep, "cu_keep", device, (rows + 1,))
+    if dst_start is not None:
+        _ints(dst_start, "dst_start", device, (rows,))
+    _call("spin_kv_slots_copy", keep, stream, a, src_table.data_ptr(), src_table.shape[1], keep.data_ptr(),
+          cu_keep.data_ptr(), keep.shape[0], rows, b, dst_table.data_ptr(), dst_table.shape[1], _ptr(dst_start))
+    return dst
+
+
+def _status(out, n: int, device, stream) -> torch.Tensor:
+    if out is None:
+        return _empty((n,), torch.int32, device, stream)
+    _ints(out, "status", device, (n,))
+    return out
+
+
+def reserve_kv_pages(pool: dict, block_table: torch.Tensor, lens: torch.Tensor, add: torch.Tensor,
+                     status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Room for add[b] more slots in every row: pages are popped from the pool (alloc_kv_pages)
+    into block_table [rows, cols] and lens [rows] grows, in row order. Returns int32 [rows]:
+    KV_OK, KV_NO_PAGES (the free pages do not reach this row, which is left as it was) or
+    KV_REFUSED (bad length or count, no column left)."""
+    kv, p, device = _pool(pool, block_table, lens)
+    rows = block_table.shape[0]
+    _ints(add, "add", device, (rows,))
+    status = _status(status, rows, device, stream)
+    _call("spin_kv_pages_reserve", lens, stream, kv, p, block_table.data_ptr(), rows, block_table.shape[1],
+          lens.data_ptr(), add.data_ptr(), status.data_ptr())
+    return status
+
+
+def fork_kv_pages(pool: dict, block_table: torch.Tensor, lens: torch.Tensor, parents: torch.Tensor,
+                  children: torch.Tensor, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Fork rows parents[i] into the empty rows children[i]: full pages are shared (refs + 1), the
+    filled slots of a partly filled last page are copied into a page of the child's own. Returns
+    int32 [n]: KV_OK, KV_NO_PAGES, or KV_REFUSED (bad index, a child that is not empty or was
+    claimed by an earlier fork of the call)."""
+    kv, p, device = _pool(pool, block_table, lens)
+    _ints(parents, "parents", device, (-1,))
+    n = parents.shape[0]
+    _ints(children, "children", device, (n,))
+    status = _status(status, n, device, stream)
+    _call("spin_kv_pages_fork", lens, stream, kv, p, block_table.data_ptr(), block_table.shape[0],
+          block_table.shape[1], lens.data_ptr(), parents.data_ptr(), children.data_ptr(), n, status.data_ptr())
+    return status
+
+
+def free_kv_pages(pool: dict, block_table: torch.Tensor, lens: torch.Tensor, rows: torch.Tensor, stream=None) -> None:
+    """Let the listed rows (int32 [n]) go: their pages' refs fall by one, their columns become -1
+    and their lengths 0, and pages nobody holds any more return to the pool in ascending order."""
+    kv, p, device = _pool(pool, block_table, lens)
+    _ints(rows, "rows", device, (-1,))
+    _call("spin_kv_pages_free", lens, stream, kv, p, block_table.data_ptr(), block_table.shape[0],
+          block_table.shape[1], lens.data_ptr(), rows.data_ptr(), rows.shape[0])
 
 
 def dequant_hadamard_inverse(codes: torch.Tensor, n: int, scale: torch.Tensor, zero: torch.Tensor | None = None,

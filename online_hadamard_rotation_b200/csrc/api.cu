@@ -124,6 +124,34 @@ static spin_status_t hadamard_quant(const void *x_bf16, int64_t tokens, int32_t 
                                          reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// A cache in pages: its geometry first (SPIN_ERR_UNSUPPORTED_SIZE), then its pointers. A page's
+// rows (n_kv_heads x page_size) are bounded so that offsets inside a page fit 32 bits.
+static spin_status_t check_pages(const spin_kv_pages_t *c) {
+  if (!c || c->pages < 0 || c->n_kv_heads <= 0 || c->page_size <= 0) return SPIN_ERR_INVALID_ARG;
+  if (c->head_dim != 128 || (int64_t)c->n_kv_heads * c->page_size > (1 << 24)) return SPIN_ERR_UNSUPPORTED_SIZE;
+  return SPIN_OK;
+}
+static spin_status_t check_pages_memory(const spin_kv_pages_t *c) {
+  if (!c->k_cache || !c->v_cache || !c->k_scale || !c->k_zero || !c->v_scale || !c->v_zero)
+    return SPIN_ERR_INVALID_ARG;
+  if (!aligned(c->k_cache, 16) || !aligned(c->v_cache, 16) || !aligned(c->k_scale, 16) || !aligned(c->k_zero, 16) ||
+      !aligned(c->v_scale, 16) || !aligned(c->v_zero, 16))
+    return SPIN_ERR_MISALIGNED;
+  return SPIN_OK;
+}
+static KvPages kv_pages(const spin_kv_pages_t *c) {
+  return KvPages{c->k_cache, c->v_cache, c->k_scale, c->k_zero, c->v_scale, c->v_zero, c->pages, c->n_kv_heads,
+                 c->page_size};
+}
+// A pool and the table it serves, for the reserve, fork and free entry points.
+static spin_status_t check_pool(const spin_kv_pool_t *pool, const int32_t *table, const int32_t *lens) {
+  if (!pool || !pool->refs || !pool->free_pages || !pool->free_count || !table || !lens) return SPIN_ERR_INVALID_ARG;
+  if (!aligned(pool->refs, 4) || !aligned(pool->free_pages, 4) || !aligned(pool->free_count, 4) ||
+      !aligned(table, 4) || !aligned(lens, 4))
+    return SPIN_ERR_MISALIGNED;
+  return SPIN_OK;
+}
+
 extern "C" {
 
 spin_status_t spin_hadamard_quant_int4_ex(const void *x_bf16, int64_t tokens, int32_t n, float clip,
@@ -259,6 +287,143 @@ spin_status_t spin_dequant_hadamard_inverse(const uint8_t *codes, int64_t rows, 
   if (st != SPIN_OK) return st;
   return cuda_status(launch_dequant_inverse(codes, rows, log_n, mode, scale, zero, sign_bits, flags, out,
                                             out_dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t spin_paged_attention_workspace_bytes(int32_t n_q_heads, int32_t n_kv_heads, int32_t max_q_len) {
+  if (n_q_heads <= 0 || n_kv_heads <= 0 || max_q_len <= 0 || n_q_heads % n_kv_heads != 0) return 0;
+  return paged_attention_workspace_bytes(n_q_heads / n_kv_heads, max_q_len);
+}
+
+spin_status_t spin_paged_attention_int4kv(const void *q, int32_t tokens, const spin_kv_pages_t *cache,
+                                          const int32_t *block_table, int32_t seqs, int32_t table_cols,
+                                          const int32_t *lens, const int32_t *cu_q, int32_t max_q_len,
+                                          int32_t n_q_heads, float softmax_scale, int32_t window, int32_t sinks,
+                                          void *out, int32_t out_dtype, void *workspace, size_t workspace_bytes,
+                                          spin_stream_t stream) {
+  spin_status_t st = check_pages(cache);
+  if (st != SPIN_OK) return st;
+  if (tokens < 0 || seqs < 0 || table_cols < 1 || max_q_len < 1 || n_q_heads <= 0 ||
+      n_q_heads % cache->n_kv_heads != 0 || (!cu_q && tokens != seqs) || !(softmax_scale > 0.0f) ||
+      !std::isfinite(softmax_scale) || window < 0 || sinks < 0 || (out_dtype != SPIN_BF16 && out_dtype != SPIN_F32))
+    return SPIN_ERR_INVALID_ARG;
+  const int page = cache->page_size;
+  if (page < 16 || page > 65536 || (page & (page - 1)) != 0 || n_q_heads > 65535 ||
+      (int64_t)tokens * n_q_heads >= (int64_t(1) << 31))
+    return SPIN_ERR_UNSUPPORTED_SIZE;
+  if (seqs == 0 || tokens == 0) return SPIN_OK;
+  if (!q || !block_table || !lens || !out || !workspace ||
+      workspace_bytes < spin_paged_attention_workspace_bytes(n_q_heads, cache->n_kv_heads, max_q_len))
+    return SPIN_ERR_INVALID_ARG;
+  if ((st = check_pages_memory(cache)) != SPIN_OK) return st;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || !aligned(block_table, 4) ||
+      !aligned(lens, 4) || (cu_q && !aligned(cu_q, 4)))
+    return SPIN_ERR_MISALIGNED;
+  if ((st = check_device()) != SPIN_OK) return st;
+  PagedAttention p;
+  p.q = q;
+  p.kv = kv_pages(cache);
+  p.block_table = block_table;
+  p.lens = lens;
+  p.cu_q = cu_q;
+  p.tokens = tokens;
+  p.seqs = seqs;
+  p.table_cols = table_cols;
+  p.n_q_heads = n_q_heads;
+  p.max_q_len = max_q_len;
+  p.window = window;
+  p.sinks = sinks;
+  p.softmax_scale = softmax_scale;
+  p.out = out;
+  p.out_f32 = out_dtype == SPIN_F32;
+  p.workspace = workspace;
+  return cuda_status(launch_paged_attention(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+spin_status_t spin_kv_pages_copy(const spin_kv_pages_t *src, const int32_t *src_pages, const spin_kv_pages_t *dst,
+                                 const int32_t *dst_pages, int32_t n, spin_stream_t stream) {
+  spin_status_t st = check_pages(src);
+  if (st == SPIN_OK) st = check_pages(dst);
+  if (st != SPIN_OK) return st;
+  if (src->n_kv_heads != dst->n_kv_heads || src->page_size != dst->page_size) return SPIN_ERR_UNSUPPORTED_SIZE;
+  if (n < 0) return SPIN_ERR_INVALID_ARG;
+  if (n == 0) return SPIN_OK;
+  if (!src_pages || !dst_pages) return SPIN_ERR_INVALID_ARG;
+  if ((st = check_pages_memory(src)) != SPIN_OK || (st = check_pages_memory(dst)) != SPIN_OK) return st;
+  if (!aligned(src_pages, 4) || !aligned(dst_pages, 4)) return SPIN_ERR_MISALIGNED;
+  // the grid's x limit, at 2048 pieces of 16 bytes a block
+  if ((int64_t)n * src->n_kv_heads * src->page_size > (int64_t(1) << 40)) return SPIN_ERR_UNSUPPORTED_SIZE;
+  if ((st = check_device()) != SPIN_OK) return st;
+  return cuda_status(launch_kv_pages_copy(kv_pages(src), src_pages, kv_pages(dst), dst_pages, n,
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+spin_status_t spin_kv_slots_copy(const spin_kv_pages_t *src, const int32_t *src_table, int32_t src_cols,
+                                 const int32_t *keep, const int32_t *cu_keep, int32_t n, int32_t rows,
+                                 const spin_kv_pages_t *dst, const int32_t *dst_table, int32_t dst_cols,
+                                 const int32_t *dst_start, spin_stream_t stream) {
+  spin_status_t st = check_pages(src);
+  if (st == SPIN_OK) st = check_pages(dst);
+  if (st != SPIN_OK) return st;
+  if (src->n_kv_heads != dst->n_kv_heads) return SPIN_ERR_UNSUPPORTED_SIZE;
+  if (n < 0 || rows < 0 || src_cols < 1 || dst_cols < 1) return SPIN_ERR_INVALID_ARG;
+  if (n == 0 || rows == 0) return SPIN_OK;
+  if (!src_table || !dst_table || !keep || !cu_keep) return SPIN_ERR_INVALID_ARG;
+  if ((st = check_pages_memory(src)) != SPIN_OK || (st = check_pages_memory(dst)) != SPIN_OK) return st;
+  if (!aligned(src_table, 4) || !aligned(dst_table, 4) || !aligned(keep, 4) || !aligned(cu_keep, 4) ||
+      (dst_start && !aligned(dst_start, 4)))
+    return SPIN_ERR_MISALIGNED;
+  if ((st = check_device()) != SPIN_OK) return st;
+  return cuda_status(launch_kv_slots_copy(kv_pages(src), src_table, src_cols, keep, cu_keep, n, rows, kv_pages(dst),
+                                          dst_table, dst_cols, dst_start, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+spin_status_t spin_kv_pages_reserve(const spin_kv_pages_t *cache, const spin_kv_pool_t *pool, int32_t *block_table,
+                                    int32_t rows, int32_t table_cols, int32_t *lens, const int32_t *add,
+                                    int32_t *status, spin_stream_t stream) {
+  spin_status_t st = check_pages(cache);
+  if (st != SPIN_OK) return st;
+  if (rows < 0 || table_cols < 1) return SPIN_ERR_INVALID_ARG;
+  if (rows == 0) return SPIN_OK;
+  if (!add || !status) return SPIN_ERR_INVALID_ARG;
+  if ((st = check_pool(pool, block_table, lens)) != SPIN_OK) return st;
+  if (!aligned(add, 4) || !aligned(status, 4)) return SPIN_ERR_MISALIGNED;
+  if ((st = check_device()) != SPIN_OK) return st;
+  return cuda_status(launch_kv_pages_reserve(kv_pages(cache), KvPool{pool->refs, pool->free_pages, pool->free_count},
+                                             block_table, rows, table_cols, lens, add, status,
+                                             reinterpret_cast<cudaStream_t>(stream)));
+}
+
+spin_status_t spin_kv_pages_fork(const spin_kv_pages_t *cache, const spin_kv_pool_t *pool, int32_t *block_table,
+                                 int32_t rows, int32_t table_cols, int32_t *lens, const int32_t *parents,
+                                 const int32_t *children, int32_t n, int32_t *status, spin_stream_t stream) {
+  spin_status_t st = check_pages(cache);
+  if (st != SPIN_OK) return st;
+  if (rows < 0 || table_cols < 1 || n < 0) return SPIN_ERR_INVALID_ARG;
+  if (n == 0) return SPIN_OK;
+  if (!parents || !children || !status) return SPIN_ERR_INVALID_ARG;
+  if ((st = check_pool(pool, block_table, lens)) != SPIN_OK) return st;
+  if ((st = check_pages_memory(cache)) != SPIN_OK) return st;
+  if (!aligned(parents, 4) || !aligned(children, 4) || !aligned(status, 4)) return SPIN_ERR_MISALIGNED;
+  if ((st = check_device()) != SPIN_OK) return st;
+  return cuda_status(launch_kv_pages_fork(kv_pages(cache), KvPool{pool->refs, pool->free_pages, pool->free_count},
+                                          block_table, rows, table_cols, lens, parents, children, n, status,
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+spin_status_t spin_kv_pages_free(const spin_kv_pages_t *cache, const spin_kv_pool_t *pool, int32_t *block_table,
+                                 int32_t rows, int32_t table_cols, int32_t *lens, const int32_t *list, int32_t n,
+                                 spin_stream_t stream) {
+  spin_status_t st = check_pages(cache);
+  if (st != SPIN_OK) return st;
+  if (rows < 0 || table_cols < 1 || n < 0) return SPIN_ERR_INVALID_ARG;
+  if (n == 0) return SPIN_OK;
+  if (!list) return SPIN_ERR_INVALID_ARG;
+  if ((st = check_pool(pool, block_table, lens)) != SPIN_OK) return st;
+  if (!aligned(list, 4)) return SPIN_ERR_MISALIGNED;
+  if ((st = check_device()) != SPIN_OK) return st;
+  return cuda_status(launch_kv_pages_free(kv_pages(cache), KvPool{pool->refs, pool->free_pages, pool->free_count},
+                                          block_table, rows, table_cols, lens, list, n,
+                                          reinterpret_cast<cudaStream_t>(stream)));
 }
 
 void spin_test_stall_tensor_core_waits(int enable) { set_stall_test(enable); }

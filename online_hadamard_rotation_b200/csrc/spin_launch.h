@@ -48,6 +48,43 @@ cudaError_t launch_decode_attention(const void *q, const uint8_t *k_cache, const
                                     const void *v_zero, const int32_t *lens, int batch, int n_q_heads,
                                     int n_kv_heads, int cache_len, float softmax_scale, void *out, bool out_f32,
                                     float *workspace, cudaStream_t stream);
+// The INT4 KV cache in pages and its pool (spin_kv_pages_t, spin_kv_pool_t), and the copies and
+// table operations of k7_kv_pages.cu. Sizes are positive and checked by the entry points.
+struct KvPages {
+  uint8_t *k_cache, *v_cache;
+  void *k_scale, *k_zero, *v_scale, *v_zero;
+  int pages, n_kv_heads, page_size;
+};
+struct KvPool {
+  int32_t *refs, *free_pages, *free_count;
+};
+cudaError_t launch_kv_pages_copy(const KvPages &src, const int32_t *src_pages, const KvPages &dst,
+                                 const int32_t *dst_pages, int n, cudaStream_t stream);
+cudaError_t launch_kv_slots_copy(const KvPages &src, const int32_t *src_table, int src_cols, const int32_t *keep,
+                                 const int32_t *cu_keep, int n, int rows, const KvPages &dst,
+                                 const int32_t *dst_table, int dst_cols, const int32_t *dst_start,
+                                 cudaStream_t stream);
+cudaError_t launch_kv_pages_reserve(const KvPages &kv, const KvPool &pool, int32_t *table, int rows, int cols,
+                                    int32_t *lens, const int32_t *add, int32_t *status, cudaStream_t stream);
+cudaError_t launch_kv_pages_fork(const KvPages &kv, const KvPool &pool, int32_t *table, int rows, int cols,
+                                 int32_t *lens, const int32_t *parents, const int32_t *children, int n,
+                                 int32_t *status, cudaStream_t stream);
+cudaError_t launch_kv_pages_free(const KvPages &kv, const KvPool &pool, int32_t *table, int rows, int cols,
+                                 int32_t *lens, const int32_t *list, int n, cudaStream_t stream);
+// Attention over the INT4 KV cache in pages (k6_paged_attn.cu). Pointers and sizes as
+// spin_paged_attention_int4kv's, already checked.
+struct PagedAttention {
+  const void *q;
+  KvPages kv;
+  const int32_t *block_table, *lens, *cu_q;
+  int tokens, seqs, table_cols, n_q_heads, max_q_len, window, sinks;
+  float softmax_scale;
+  void *out;
+  bool out_f32;
+  void *workspace;
+};
+size_t paged_attention_workspace_bytes(int group, int max_q_len);
+cudaError_t launch_paged_attention(const PagedAttention &p, cudaStream_t stream);
 // W4A4 GEMM on packed INT4 codes (k5_w4a4_gemm.cu): shapes it takes (n_out a multiple
 // of 256, k a multiple of 128 up to 65536), the launch, and its status word.
 bool w4a4_shape_supported(int64_t tokens, int n_out, int k);

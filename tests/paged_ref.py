@@ -1,0 +1,168 @@
+"""Binary64 statements of the paged INT4 KV cache's operators, for the tests: attention over
+block tables, and the pool's reserve, fork and free as loops over rows."""
+import math
+
+import torch
+
+CODES = ("k_cache", "v_cache")
+STEPS = ("k_scale", "k_zero", "v_scale", "v_zero")
+
+
+def random_pages(pages, hkv, page, seed, device="cuda"):
+    """Random codes, scales near those of normal data and whole zeros."""
+    g = torch.Generator(device="cpu").manual_seed(seed)
+    c = {n: torch.randint(0, 256, (pages, hkv, page, 64), generator=g, dtype=torch.uint8) for n in CODES}
+    for n in ("k_scale", "v_scale"):
+        c[n] = (0.05 + 0.4 * torch.rand((pages, hkv, page), generator=g)).half()
+    for n in ("k_zero", "v_zero"):
+        c[n] = torch.randint(0, 16, (pages, hkv, page), generator=g).half()
+    return {n: t.to(device) for n, t in c.items()}
+
+
+def attention(q, cache, table, lens, cu, scale=None, window=0, sinks=0):
+    """(out, magnitude, score magnitude): the result in binary64; per element the sum of
+    p_j s_j (|c_j - 8| + |8 - z_j|), the terms the kernel adds; the largest sum of a score's
+    term sizes. Rows outside the sequences are NaN."""
+    q, table = q.double().cpu(), table.cpu()
+    cache = {n: t.cpu() for n, t in cache.items()}
+    tokens, hq, d = q.shape
+    pages, hkv, page, _ = cache["k_cache"].shape
+    group = hq // hkv
+    scale = 1 / math.sqrt(d) if scale is None else scale
+    out = torch.full((tokens, hq, d), math.nan, dtype=torch.float64)
+    size = torch.zeros_like(out)
+    score_size = 0.0
+    for b, n in enumerate(lens):
+        n = min(max(n, 0), table.shape[1] * page)
+        nq = cu[b + 1] - cu[b]
+        slots = torch.arange(n)
+        ids = table[b, slots // page].long()
+        there = (ids >= 0) & (ids < pages)
+        ids = ids.clamp(0, pages - 1)
+
+        def rows(name):
+            codes = cache[name + "_cache"][ids, :, slots % page]  # [n, hkv, 64]
+            u = torch.stack([codes & 15, codes >> 4], -1).flatten(-2).double()
+            s = cache[name + "_scale"][ids, :, slots % page].double()[..., None]
+            z = cache[name + "_zero"][ids, :, slots % page].double()[..., None]
+            return u, s, z
+
+        (ku, ks, kz), (vu, vs, vz) = rows("k"), rows("v")
+        for i in range(nq):
+            p = n - nq + i
+            seen = there & (slots <= p)
+            if window:
+                seen &= (slots > p - window) | (slots < sinks)
+            t = cu[b] + i
+            out[t] = 0
+            at = seen.nonzero()[:, 0]
+            if not len(at):
+                continue
+            for g in range(hkv):
+                k, v = (ku[at, g] - kz[at, g]) * ks[at, g], (vu[at, g] - vz[at, g]) * vs[at, g]
+                rows_q = q[t, g * group:(g + 1) * group]
+                w = torch.softmax(rows_q @ k.T * scale, 1)
+                out[t, g * group:(g + 1) * group] = w @ v
+                size[t, g * group:(g + 1) * group] = w @ (((vu[at, g] - 8).abs() + (8 - vz[at, g]).abs()) * vs[at, g])
+                terms = (rows_q.abs() @ (ku[at, g] - 8).abs().T +
+                         rows_q.sum(1).abs()[:, None] * (8 - kz[at, g]).abs().T) * ks[at, g].T * scale
+                score_size = max(score_size, float(terms.max()))
+    return out, size, score_size
+
+
+def check_attention(got, ref, what=""):
+    """|got - out| <= eps * magnitude (+ half a bf16 step of the value).
+
+    The weights are two bf16 terms, together within 2^-17 of the fp32 value. A score is a sum of
+    exact products in fp32: at most 128 + 2 additions, each within 2^-23 of the sum of the term
+    sizes S (tensor cores truncate), but the roundings of a tree of 16-wide steps are at most
+    8 + 4 deep: 16 * 2^-23 S covers them. A weight's relative error is that of its score, and
+    enters the numerator and the sum of weights: twice. ex2's 2^-22 and the fp32 sums' few
+    2^-24 steps per block level: 2^-19 together."""
+    out, size, s = ref
+    got = got.double().cpu()
+    bf16 = what == "bf16"
+    eps = 2 ** -17 + 2 * 16 * 2 ** -23 * s + 2 ** -19
+    rows = ~torch.isnan(out[:, 0, 0])
+    tol = eps * size + (2 ** -8 * out.abs() if bf16 else 0)
+    bad = ((got - out).abs() > tol + 1e-30)[rows]
+    assert torch.isfinite(got[rows]).all()
+    assert not bad.any(), f"{int(bad.sum())} elements off, worst {float(((got - out).abs() / (tol + 1e-30))[rows].max()):.3g} x"
+
+
+class Pool:
+    """The pool's rules, one row after another."""
+
+    def __init__(self, pages, page, table, lens, refs, stack):
+        self.pages, self.page = pages, page
+        self.table, self.lens, self.refs, self.stack = table, lens, refs, stack  # lists
+
+    def reserve(self, add):
+        status, free, asked = [], len(self.stack), 0
+        cols = len(self.table[0])
+        for b, n in enumerate(add):
+            length = self.lens[b]
+            if n < 0 or length < 0 or length > cols * self.page or -(-(length + n) // self.page) > cols:
+                status.append(2)
+                continue
+            have = -(-length // self.page)
+            want = -(-(length + n) // self.page) - have
+            asked += want
+            if want and asked > free:
+                status.append(1)
+                continue
+            for j in range(want):
+                page = self.stack.pop()
+                self.table[b][have + j] = page
+                self.refs[page] = 1
+            self.lens[b] = length + n
+            status.append(0)
+        return status
+
+    def fork(self, parents, children):
+        """(status, [(source page, new page, slots)])"""
+        status, copies, free, asked = [], [], len(self.stack), 0
+        lens = list(self.lens)
+        taken = set()
+        rows, cols = len(self.table), len(self.table[0])
+        for p, c in zip(parents, children):
+            if not (0 <= p < rows and 0 <= c < rows) or p == c or lens[c] != 0 or c in taken or lens[p] < 0 \
+                    or lens[p] > cols * self.page:
+                status.append(2)
+                continue
+            taken.add(c)
+            full, tail = divmod(lens[p], self.page)
+            asked += tail > 0
+            if tail and asked > free:
+                status.append(1)
+                continue
+            row = [-1] * cols
+            for j in range(full):
+                row[j] = self.table[p][j]
+                if 0 <= row[j] < self.pages:
+                    self.refs[row[j]] += 1
+            if tail:
+                row[full] = self.stack.pop()
+                self.refs[row[full]] = 1
+                copies.append((self.table[p][full], row[full], tail))
+            self.table[c], self.lens[c] = row, lens[p]
+            status.append(0)
+        return status, copies
+
+    def free(self, rows):
+        gone = []
+        for r in rows:
+            if not 0 <= r < len(self.table):
+                continue
+            if self.lens[r] <= 0:
+                self.lens[r] = 0
+                continue
+            for j in range(min(-(-self.lens[r] // self.page), len(self.table[r]))):
+                page = self.table[r][j]
+                if 0 <= page < self.pages and self.refs[page] > 0:
+                    self.refs[page] -= 1
+                    if self.refs[page] == 0:
+                        gone.append(page)
+            self.table[r] = [-1] * len(self.table[r])
+            self.lens[r] = 0
+        self.stack += sorted(gone)
