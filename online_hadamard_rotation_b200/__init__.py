@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes as C
 import os
 import re
+import struct
 
 import torch
 
@@ -44,17 +45,6 @@ KV_REFUSED = 2
 
 _STATUS = {0: "SPIN_OK", 1: "SPIN_ERR_INVALID_ARG", 2: "SPIN_ERR_UNSUPPORTED_SIZE",
            3: "SPIN_ERR_MISALIGNED", 4: "SPIN_ERR_CUDA", 5: "SPIN_ERR_DEVICE"}
-
-
-class _KvPages(C.Structure):
-    """spin_kv_pages_t"""
-    _fields_ = [(n, C.c_void_p) for n in ("k_cache", "v_cache", "k_scale", "k_zero", "v_scale", "v_zero")] + \
-        [(n, C.c_int32) for n in ("pages", "n_kv_heads", "page_size", "head_dim")]
-
-
-class _KvPool(C.Structure):
-    """spin_kv_pool_t"""
-    _fields_ = [(n, C.c_void_p) for n in ("refs", "free_pages", "free_count")]
 
 
 class SpinError(RuntimeError):
@@ -92,7 +82,7 @@ def lib() -> C.CDLL:
     L.spin_w4a4_gemm.argtypes = [vp, vp, i64, vp, vp, i32, i32, vp, i32, vp]
     L.spin_decode_attention_workspace_bytes.argtypes = [i32, i32, i32]
     L.spin_decode_attention_workspace_bytes.restype = C.c_size_t
-    kv, pool = C.POINTER(_KvPages), C.POINTER(_KvPool)
+    kv = pool = C.c_char_p  # packed spin_kv_pages_t and spin_kv_pool_t
     L.spin_paged_attention_int4kv.argtypes = [vp, i32, kv, vp, i32, i32, vp, vp, i32, i32, f32, i32, i32, vp, i32, vp,
                                               C.c_size_t, vp]
     L.spin_paged_attention_workspace_bytes.argtypes = [i32, i32, i32]
@@ -470,33 +460,32 @@ def decode_attention_int4kv(q: torch.Tensor, cache: dict, lens: torch.Tensor, so
 
 
 # ------------------------------------------------------------------ the INT4 KV cache in pages
-_KV_CODES = ("k_cache", "v_cache")
-_KV_STEPS = ("k_scale", "k_zero", "v_scale", "v_zero")
+# These calls are a few microseconds of device work at decode sizes, so the checks below are
+# written to cost little: one pass over each tensor, no objects made on the way.
+_U8, _F16, _I32 = torch.uint8, torch.float16, torch.int32
+_KV_ARRAYS = (("k_cache", _U8), ("v_cache", _U8), ("k_scale", _F16), ("k_zero", _F16), ("v_scale", _F16),
+              ("v_zero", _F16))
+_pack_pages = struct.Struct("6P4i").pack  # spin_kv_pages_t
+_pack_pool = struct.Struct("3P").pack     # spin_kv_pool_t
+# the current stream's handle without a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _device_of(t: torch.Tensor, stream):
-    """The stream a call runs on, with its device made current if it is not: (stream handle,
-    device to go back to or None)."""
-    if stream is None:
-        stream = torch.cuda.current_stream(t.device)
-    now = torch.cuda.current_device()
-    if t.device.index != now:
-        torch.cuda.set_device(t.device)
-        return stream.cuda_stream, now
-    return stream.cuda_stream, None
+def _call(fn: str, device: int, stream, *args) -> None:
+    """Run a library entry point on device index `device`, on its current (or the given) stream."""
+    handle = _raw_stream(device) if stream is None else stream.cuda_stream
+    back = torch.cuda.current_device()
+    if back == device:
+        st = getattr(lib(), fn)(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            st = getattr(lib(), fn)(*args, handle)
+    if st != 0:
+        _check(fn, st)
 
 
-def _call(fn: str, t: torch.Tensor, stream, *args) -> None:
-    """Run a library entry point on `t`'s device and its current (or the given) stream."""
-    handle, back = _device_of(t, stream)
-    try:
-        _check(fn, getattr(lib(), fn)(*args, handle))
-    finally:
-        if back is not None:
-            torch.cuda.set_device(back)
-
-
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
+def _empty(shape, dtype, device: int, stream) -> torch.Tensor:
     """A tensor the call on `stream` writes: the caching allocator orders a block's reuse on the
     stream it was made on, so it is made on that one."""
     if stream is None:
@@ -505,47 +494,63 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _ints(t: torch.Tensor, name: str, device, shape) -> None:
-    """A contiguous int32 CUDA tensor of the given shape (-1: any size) on the cache's device."""
-    if t.dtype != torch.int32:
+def _refuse(t: torch.Tensor, name: str, device: int, want: str) -> None:
+    if t.dtype is not _I32:
         raise TypeError(f"{name}: expected torch.int32, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.dim() != len(shape) or any(n not in (-1, m) for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name}: expected shape {want}, got {tuple(t.shape)}")
 
 
-def _pages(cache: dict, what: str = "cache") -> _KvPages:
+def _vec(t: torch.Tensor, name: str, device: int, n: int) -> int:
+    """Check a contiguous int32 CUDA tensor [n] on the cache's device and return its pointer.
+    Callers keep the tensor bound until the launch: an argument that nothing else holds would be
+    freed, and its memory handed to the call's own outputs."""
+    if t.dtype is not _I32 or t.numel() != n or t.dim() != 1 or t.get_device() != device or not t.is_contiguous():
+        _refuse(t, name, device, f"({n},)")
+    return t.data_ptr()
+
+
+def _table(t: torch.Tensor, name: str, device: int):
+    """(pointer, rows, cols) of a block table, checked like _vec."""
+    if t.dtype is not _I32 or t.dim() != 2 or t.get_device() != device or not t.is_contiguous():
+        _refuse(t, name, device, "[rows, cols]")
+    rows, cols = t.shape
+    return t.data_ptr(), rows, cols
+
+
+def _pages(cache: dict, what: str = "cache"):
     """Check a cache dict ([pages, n_kv_heads, page_size, d/2] codes, [pages, n_kv_heads,
-    page_size] fp16 scales and zeros) and describe it for the library."""
-    k = cache["k_cache"]
-    if k.dim() != 4:
-        raise ValueError(f"{what}: k_cache is [pages, n_kv_heads, page_size, head_dim / 2], got {tuple(k.shape)}")
-    device, shape = k.device, k.shape
-    if not k.is_cuda:
+    page_size] fp16 scales and zeros): (packed spin_kv_pages_t, device index, shape of k_cache)."""
+    shape = cache["k_cache"].shape
+    if len(shape) != 4:
+        raise ValueError(f"{what}: k_cache is [pages, n_kv_heads, page_size, head_dim / 2], got {tuple(shape)}")
+    steps = shape[:3]
+    device = cache["k_cache"].get_device()
+    if device < 0:
         raise ValueError(f"{what}: k_cache must be a CUDA tensor")
     ptrs = []
-    for names, dtype, want in ((_KV_CODES, torch.uint8, shape), (_KV_STEPS, torch.float16, shape[:3])):
-        for name in names:
-            t = cache[name]
-            if t.dtype != dtype:
-                raise TypeError(f"{what}: {name}: expected {dtype}, got {t.dtype}")
-            if t.device != device or t.shape != want or not t.is_contiguous():
-                raise ValueError(f"{what}: {name} must be a contiguous {tuple(want)} tensor on {device}")
-            ptrs.append(t.data_ptr())
-    return _KvPages(*ptrs, shape[0], shape[1], shape[2], 2 * shape[3])
+    for name, dtype in _KV_ARRAYS:
+        t = cache[name]
+        if t.dtype is not dtype:
+            raise TypeError(f"{what}: {name}: expected {dtype}, got {t.dtype}")
+        if t.shape != (shape if dtype is _U8 else steps) or t.get_device() != device or not t.is_contiguous():
+            raise ValueError(f"{what}: {name} must be a contiguous {tuple(shape if dtype is _U8 else steps)} tensor "
+                             f"on cuda:{device}")
+        ptrs.append(t.data_ptr())
+    return _pack_pages(*ptrs, shape[0], shape[1], shape[2], 2 * shape[3]), device, shape
 
 
 def _pool(pool: dict, block_table: torch.Tensor, lens: torch.Tensor):
-    kv = _pages(pool, "pool")
-    device, pages = pool["k_cache"].device, pool["k_cache"].shape[0]
-    for name, n in (("refs", pages), ("free_pages", pages), ("free_count", 1)):
-        _ints(pool[name], name, device, (n,))
-    _ints(block_table, "block_table", device, (-1, -1))
-    _ints(lens, "lens", device, (block_table.shape[0],))
-    return kv, _KvPool(pool["refs"].data_ptr(), pool["free_pages"].data_ptr(), pool["free_count"].data_ptr()), device
+    """(packed cache, packed pool, device index, table pointer, rows, cols, lens pointer)"""
+    kv, device, shape = _pages(pool, "pool")
+    packed = _pack_pool(_vec(pool["refs"], "refs", device, shape[0]),
+                        _vec(pool["free_pages"], "free_pages", device, shape[0]),
+                        _vec(pool["free_count"], "free_count", device, 1))
+    table, rows, cols = _table(block_table, "block_table", device)
+    return kv, packed, device, table, rows, cols, _vec(lens, "lens", device, rows)
 
 
 def alloc_kv_pages(pages: int, n_kv_heads: int, page_size: int = 64, head_dim: int = 128, device="cuda") -> dict:
@@ -576,37 +581,41 @@ def paged_attention_int4kv(q: torch.Tensor, cache: dict, block_table: torch.Tens
     with j > p - window or j < sinks. Returns out [tokens, hq, d] (fp32 or bf16); rows of a given
     `out` behind the last sequence are left as they were. `workspace` (uint8, at least
     paged_attention_workspace_bytes) is allocated through torch when not given."""
-    kv = _pages(cache)
+    kv, device, shape = _pages(cache)
     if q.dim() != 3:
         raise ValueError(f"q: expected [tokens, n_q_heads, head_dim], got shape {tuple(q.shape)}")
     tokens, hq, d = q.shape
-    device = cache["k_cache"].device
-    _need(q, "q", torch.bfloat16, device, (tokens, hq, kv.head_dim))
-    _ints(block_table, "block_table", device, (-1, -1))
-    seqs, cols = block_table.shape
-    _ints(lens, "lens", device, (seqs,))
+    _rows(q, "q", torch.bfloat16, device, (tokens, hq, 2 * shape[3]))
+    table, seqs, cols = _table(block_table, "block_table", device)
+    lens_at, cu_at = _vec(lens, "lens", device, seqs), None
     if cu_q is not None:
-        _ints(cu_q, "cu_q", device, (seqs + 1,))
+        cu_at = _vec(cu_q, "cu_q", device, seqs + 1)
     elif tokens != seqs:
         raise ValueError(f"{tokens} tokens for {seqs} sequences need cu_q")
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype is not torch.float32 and out_dtype is not torch.bfloat16:
+        raise TypeError(f"out_dtype: expected torch.float32 or torch.bfloat16, got {out_dtype}")
     if out is None:
-        if out_dtype not in (torch.float32, torch.bfloat16):
-            raise TypeError(f"out_dtype: expected torch.float32 or torch.bfloat16, got {out_dtype}")
         out = _empty((tokens, hq, d), out_dtype, device, stream)
     else:
-        if out.dtype not in (torch.float32, torch.bfloat16):
-            raise TypeError(f"out: expected torch.float32 or torch.bfloat16, got {out.dtype}")
-        _need(out, "out", out.dtype, device, (tokens, hq, d))
+        _rows(out, "out", out_dtype, device, (tokens, hq, d))
     if workspace is None:
-        need = lib().spin_paged_attention_workspace_bytes(hq, kv.n_kv_heads, max_q_len)
-        workspace = _empty((max(need, 16),), torch.uint8, device, stream)
+        need = lib().spin_paged_attention_workspace_bytes(hq, shape[1], max_q_len)
+        workspace = _empty((max(need, 16),), _U8, device, stream)
     else:
-        _need(workspace, "workspace", torch.uint8, device)
-    scale = float(softmax_scale) if softmax_scale is not None else 1.0 / float(d) ** 0.5
-    _call("spin_paged_attention_int4kv", q, stream, q.data_ptr(), tokens, kv, block_table.data_ptr(), seqs, cols,
-          lens.data_ptr(), _ptr(cu_q), max_q_len, hq, scale, window, sinks, out.data_ptr(),
-          F32 if out.dtype == torch.float32 else BF16, workspace.data_ptr(), workspace.numel())
+        _rows(workspace, "workspace", _U8, device, workspace.shape)
+    _call("spin_paged_attention_int4kv", device, stream, q.data_ptr(), tokens, kv, table, seqs, cols, lens_at, cu_at,
+          max_q_len, hq, d ** -0.5 if softmax_scale is None else softmax_scale, window, sinks, out.data_ptr(),
+          F32 if out_dtype is torch.float32 else BF16, workspace.data_ptr(), workspace.numel())
     return out
+
+
+def _rows(t: torch.Tensor, name: str, dtype, device: int, shape) -> None:
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.get_device() != device or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor on cuda:{device}")
 
 
 def copy_kv_pages(src: dict, src_pages: torch.Tensor, dst_pages: torch.Tensor, dst: dict | None = None,
@@ -614,15 +623,16 @@ def copy_kv_pages(src: dict, src_pages: torch.Tensor, dst_pages: torch.Tensor, d
     """Page dst_pages[i] of `dst` (default: `src` itself) <- page src_pages[i] of `src`, codes,
     scales and zeros; int32 [n] ids, pairs with an id out of range are skipped. No page may be
     source and destination, or destination twice, in one call. Returns dst."""
-    dst = src if dst is None else dst
-    a, b = _pages(src, "src"), _pages(dst, "dst")
-    device = src["k_cache"].device
-    if dst["k_cache"].device != device:
-        raise ValueError(f"dst must be on {device}")
-    _ints(src_pages, "src_pages", device, (-1,))
-    _ints(dst_pages, "dst_pages", device, (src_pages.shape[0],))
-    _call("spin_kv_pages_copy", src_pages, stream, a, src_pages.data_ptr(), b, dst_pages.data_ptr(),
-          src_pages.shape[0])
+    a, device, _ = _pages(src, "src")
+    if dst is None or dst is src:
+        dst, b = src, a
+    else:
+        b, other, _ = _pages(dst, "dst")
+        if other != device:
+            raise ValueError(f"dst must be on cuda:{device}")
+    n = src_pages.numel()
+    _call("spin_kv_pages_copy", device, stream, a, _vec(src_pages, "src_pages", device, n), b,
+          _vec(dst_pages, "dst_pages", device, n), n)
     return dst
 
 
@@ -633,26 +643,25 @@ def copy_kv_slots(src: dict, src_table: torch.Tensor, keep: torch.Tensor, cu_kee
     size, or appending the slots of a small contiguous cache (its own table is one page per row:
     torch.arange(rows)[:, None]). Tables [rows, cols], keep [n], cu_keep [rows + 1], dst_start
     [rows] (None: 0), all int32. Destination slots must not be source slots. Returns dst."""
-    a, b = _pages(src, "src"), _pages(dst, "dst")
-    device = src["k_cache"].device
-    if dst["k_cache"].device != device:
-        raise ValueError(f"dst must be on {device}")
-    _ints(src_table, "src_table", device, (-1, -1))
-    rows = src_table.shape[0]
-    _ints(dst_table, "dst_table", device, (rows, -1))
-    _ints(keep, "keep", device, (-1,))
-    _ints(cu_keep, "cu_keep", device, (rows + 1,))
-    if dst_start is not None:
-        _ints(dst_start, "dst_start", device, (rows,))
-    _call("spin_kv_slots_copy", keep, stream, a, src_table.data_ptr(), src_table.shape[1], keep.data_ptr(),
-          cu_keep.data_ptr(), keep.shape[0], rows, b, dst_table.data_ptr(), dst_table.shape[1], _ptr(dst_start))
+    a, device, _ = _pages(src, "src")
+    b, other, _ = (a, device, None) if dst is src else _pages(dst, "dst")
+    if other != device:
+        raise ValueError(f"dst must be on cuda:{device}")
+    src_at, rows, src_cols = _table(src_table, "src_table", device)
+    dst_at, dst_rows, dst_cols = _table(dst_table, "dst_table", device)
+    if dst_rows != rows:
+        raise ValueError(f"dst_table: expected {rows} rows, got {dst_rows}")
+    n = keep.numel()
+    _call("spin_kv_slots_copy", device, stream, a, src_at, src_cols, _vec(keep, "keep", device, n),
+          _vec(cu_keep, "cu_keep", device, rows + 1), n, rows, b, dst_at, dst_cols,
+          None if dst_start is None else _vec(dst_start, "dst_start", device, rows))
     return dst
 
 
-def _status(out, n: int, device, stream) -> torch.Tensor:
+def _status(out, n: int, device: int, stream) -> torch.Tensor:
     if out is None:
-        return _empty((n,), torch.int32, device, stream)
-    _ints(out, "status", device, (n,))
+        return _empty((n,), _I32, device, stream)
+    _vec(out, "status", device, n)
     return out
 
 
@@ -662,12 +671,10 @@ def reserve_kv_pages(pool: dict, block_table: torch.Tensor, lens: torch.Tensor, 
     into block_table [rows, cols] and lens [rows] grows, in row order. Returns int32 [rows]:
     KV_OK, KV_NO_PAGES (the free pages do not reach this row, which is left as it was) or
     KV_REFUSED (bad length or count, no column left)."""
-    kv, p, device = _pool(pool, block_table, lens)
-    rows = block_table.shape[0]
-    _ints(add, "add", device, (rows,))
-    status = _status(status, rows, device, stream)
-    _call("spin_kv_pages_reserve", lens, stream, kv, p, block_table.data_ptr(), rows, block_table.shape[1],
-          lens.data_ptr(), add.data_ptr(), status.data_ptr())
+    kv, p, device, table, n, cols, lens_at = _pool(pool, block_table, lens)
+    add_at = _vec(add, "add", device, n)
+    status = _status(status, n, device, stream)
+    _call("spin_kv_pages_reserve", device, stream, kv, p, table, n, cols, lens_at, add_at, status.data_ptr())
     return status
 
 
@@ -677,23 +684,23 @@ def fork_kv_pages(pool: dict, block_table: torch.Tensor, lens: torch.Tensor, par
     filled slots of a partly filled last page are copied into a page of the child's own. Returns
     int32 [n]: KV_OK, KV_NO_PAGES, or KV_REFUSED (bad index, a child that is not empty or was
     claimed by an earlier fork of the call)."""
-    kv, p, device = _pool(pool, block_table, lens)
-    _ints(parents, "parents", device, (-1,))
-    n = parents.shape[0]
-    _ints(children, "children", device, (n,))
+    kv, p, device, table, rows, cols, lens_at = _pool(pool, block_table, lens)
+    n = parents.numel()
+    parents_at = _vec(parents, "parents", device, n)
+    children_at = _vec(children, "children", device, n)
     status = _status(status, n, device, stream)
-    _call("spin_kv_pages_fork", lens, stream, kv, p, block_table.data_ptr(), block_table.shape[0],
-          block_table.shape[1], lens.data_ptr(), parents.data_ptr(), children.data_ptr(), n, status.data_ptr())
+    _call("spin_kv_pages_fork", device, stream, kv, p, table, rows, cols, lens_at, parents_at, children_at, n,
+          status.data_ptr())
     return status
 
 
 def free_kv_pages(pool: dict, block_table: torch.Tensor, lens: torch.Tensor, rows: torch.Tensor, stream=None) -> None:
     """Let the listed rows (int32 [n]) go: their pages' refs fall by one, their columns become -1
     and their lengths 0, and pages nobody holds any more return to the pool in ascending order."""
-    kv, p, device = _pool(pool, block_table, lens)
-    _ints(rows, "rows", device, (-1,))
-    _call("spin_kv_pages_free", lens, stream, kv, p, block_table.data_ptr(), block_table.shape[0],
-          block_table.shape[1], lens.data_ptr(), rows.data_ptr(), rows.shape[0])
+    kv, p, device, table, n, cols, lens_at = _pool(pool, block_table, lens)
+    listed = rows.numel()
+    _call("spin_kv_pages_free", device, stream, kv, p, table, n, cols, lens_at, _vec(rows, "rows", device, listed),
+          listed)
 
 
 def dequant_hadamard_inverse(codes: torch.Tensor, n: int, scale: torch.Tensor, zero: torch.Tensor | None = None,

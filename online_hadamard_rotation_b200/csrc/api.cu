@@ -308,7 +308,8 @@ spin_status_t spin_paged_attention_int4kv(const void *q, int32_t tokens, const s
     return SPIN_ERR_INVALID_ARG;
   const int page = cache->page_size;
   if (page < 16 || page > 65536 || (page & (page - 1)) != 0 || n_q_heads > 65535 ||
-      (int64_t)tokens * n_q_heads >= (int64_t(1) << 31))
+      (int64_t)tokens * n_q_heads >= (int64_t(1) << 31) ||
+      (int64_t)cache->pages * cache->n_kv_heads * page >= (int64_t(1) << 31))
     return SPIN_ERR_UNSUPPORTED_SIZE;
   if (seqs == 0 || tokens == 0) return SPIN_OK;
   if (!q || !block_table || !lens || !out || !workspace ||

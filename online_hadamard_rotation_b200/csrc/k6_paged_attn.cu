@@ -11,26 +11,26 @@
 //   score_j = scale (q_h . khat_j),  out_h = sum_j softmax(score)_j vhat_j,
 //   khat_j = (c_j - z_j) s_j and vhat_j likewise from the slot's codes, zero and scale.
 //
-// Products run on the integers c - y, exact in fp16, y the four bits of z rounded to a whole
-// number (z itself for the whole zeros 0 .. 15 that the R3 kernel writes):
-//   q . khat   = s (q . (c - y) + (y - z) sum(q))
-//   sum_j p_j vhat_j = sum_j w_j (c_j - y_j) + sum_j w_j (y_j - z_j),  w_j = p_j s_j
-// A nibble u in bits 0-3 or 4-7 of a half is the fp16 subnormal u 2^-24 or u 2^-20: one AND and
-// one packed FMA (times 2^15 or 2^11, minus y 2^-9) give (u - y) 2^-9 exactly, and the 2^9 leaves
-// with the row's factor (scores) or at the end (values). A masked
-// slot's stale zero is four bits too, so no NaN enters a product. (A constant in y's place would
-// save a little and cost digits: with an outlier in a value row most codes sit at the zero, far
-// from any constant, and the terms to cancel outgrow the result; measured 5e-5 of the norm on
-// 65537 slots.) A query row is scaled by a power of two to a largest value of 2^14 .. 2^15, so its
+// Products run on small integers, exact in fp16. A nibble u in bits 0-3 or 4-7 of a half is the
+// fp16 subnormal u 2^-24 or u 2^-20, so one AND makes two factors of a matrix product:
+//   keys:    q . khat = s (q . c - z sum(q)), the codes as they are, the 2^-20's factor 16 taken
+//            out of the queries that meet it. Both terms are of the size of the result's parts.
+//   values:  sum_j p_j vhat_j = sum_j w_j (c_j - y_j) + sum_j w_j (y_j - z_j), w_j = p_j s_j, with y
+//            the four bits of z rounded to a whole number (z itself for the whole zeros 0 .. 15
+//            that the R3 kernel writes): one packed FMA after the AND gives (u - y) 2^-9. Without
+//            it (or with a constant in y's place) the terms to cancel can outgrow the result: with
+//            an outlier in a value row most codes sit at the zero; measured 5e-5 of the norm on
+//            65537 slots. A masked slot's stale zero is four bits too, so no NaN enters a product.
+// A query row is scaled by a power of two to a largest value of 2^14 .. 2^15, so its
 // bf16 values are exact in fp16 down to 2^-39 of the largest: the products of the scores are
-// exact. w is the sum of two fp16 terms (22 bits; one bf16 term would add as much error as a
-// bf16 result's own rounding), its reference chosen so that it stays below 2^15 whatever the
-// value scales. Sums are fp32.
+// exact. w is one fp16 term (half a step is 2^-12 of it, an eighth of the bf16 result's own
+// rounding; a bf16 term would match that), for fp32 results two (2^-23); its reference is chosen so
+// that it stays below 2^15 whatever the value scales. Sums are fp32.
 //
 // The matrices are transposed against the usual form: slots (keys) and head elements
 // (values) are the M side of mma.m16n8k16 and the query rows the N side, so that a decode
-// step with few query heads per kv head wastes little, and packed codes go from global
-// memory straight into A fragments, in registers:
+// step with few query heads per kv head wastes little, and a thread's packed codes are its own A
+// elements, expanded in registers and never written anywhere:
 //   * a row is one (token, query head) pair of a kv head, G rows per token; a row tile has
 //     R = 8 NT rows; a warp takes BS = 16 MT slots at a time
 //   * group g = lane / 4 owns slots S g .. S g + S - 1 of the block, S = 2 MT, as MMA rows (tile
@@ -41,8 +41,15 @@
 //   * values: c owns slots 2S c .. 2S c + 2S - 1, g the bytes 8g .. 8g + 7 of each: two slots'
 //     words are interleaved by byte permutes into pairs along the contraction
 //   * the weights leave the score layout [slot][row] for the B layout by movmatrix
-// The softmax keeps one reference per row that is raised only when a score exceeds it by 8
-// (weights up to 2^8 lose no relative precision), so most blocks need no cross-lane maximum.
+// Each warp keeps one block of keys and one of values in shared memory, filled by 16-byte
+// asynchronous copies that look up a page per 16 slots. The next keys are under way during the
+// softmax and the value products, the next values during the scores. Rows are padded in runs so
+// that all reads are free of bank conflicts; bulk copies of such runs (512 bytes) took 36 cycles
+// each on the copy engine and were slower. (Loads straight into registers, 32 slots a block at the same occupancy: 83 us
+// against 67 on 4 rows of up to 65537 slots, fp32.)
+// The softmax keeps one reference per row that is raised only when a weight could pass 2^14 (a
+// raised one leaves 2^9), so most blocks need no cross-lane maximum; fp16's smallest step is then
+// 2^-33 of the row's largest weight or less.
 //
 // Work is divided over a fixed number of warps: the list of all (sequence, kv head, row tile)
 // items, each as many units long as its sequence has slot blocks and kItem more for its fixed
@@ -63,6 +70,7 @@
 #include "tc_ptx.cuh"
 
 namespace spin {
+
 namespace {
 
 constexpr int kD = 128;
@@ -70,11 +78,11 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCtas = 600;  // most blocks of a launch (sets the workspace)
 constexpr int kItem = 2;       // units an item costs besides its slot blocks
-constexpr int kSnap = kItem + 1;  // cuts this close to an item's end move there
+constexpr int kSnap = 3;  // cuts this close to an item's end move there
 constexpr int kMinRun = 4;     // shortest run worth a warp of its own
 constexpr int kPart = 132;     // floats per row of a piece: 128 sums, max, sum of weights, pad
-constexpr float kRaise = 8.0f; // log2 above the reference at which it is raised
-constexpr float kRoom = 6.0f;  // a raised reference leaves weights at most 2^kRoom
+constexpr float kRoom = 9.0f;   // a raised reference leaves weights at most 2^kRoom
+constexpr float kRaise = 5.0f;  // log2 above that at which it is raised again (fp16 ends at 2^16)
 
 struct PagedArgs {
   const __nv_bfloat16 *q;
@@ -86,6 +94,7 @@ struct PagedArgs {
   float scale_log2;  // softmax scale x log2(e)
   void *out;
   float *parts;  // [grid][2][R][kPart]
+  float *heads;  // [grid][kWarps][R][kPart], read by the block that wrote them
   int4 *recs;    // [grid]
 };
 
@@ -198,24 +207,37 @@ __device__ __forceinline__ float zero_rest(uint32_t h2, int i) {
 __device__ __forceinline__ uint32_t zeros_rest(uint32_t h2) {
   return sub_f16x2(zero_bits(h2) | 0x64006400u, 0x64006400u) ^ h2;
 }
-constexpr float kCode = 512.0f;  // what the codes' 2^-9 takes out
+constexpr float kCode = 512.0f;  // what the value codes' 2^-9 takes out
+constexpr float kHalfKey = 4096.0f;  // of the key codes' 2^-24: half in the row's factor, half in the slot's
 
+// N consecutive halves of shared memory, one load.
 template <int N>
-struct HalfVec;  // 2 MT consecutive halves, one load
-template <>
-struct HalfVec<4> {
-  uint2 v;
-  __device__ __forceinline__ uint32_t word(int i) const { return i == 0 ? v.x : v.y; }
+struct HalfVec {
+  uint32_t v[N / 2];
+  __device__ __forceinline__ void load(const uint16_t *p) {
+    if constexpr (N == 8) {
+      const uint4 x = *reinterpret_cast<const uint4 *>(p);
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2 *>(p);
+      v[0] = x.x, v[1] = x.y;
+    }
+  }
+  __device__ __forceinline__ uint32_t word(int i) const { return v[i]; }
+  __device__ __forceinline__ float at(int i) const {
+    return __half2float(__ushort_as_half((unsigned short)((i & 1) ? v[i >> 1] >> 16 : v[i >> 1] & 0xFFFFu)));
+  }
 };
-template <>
-struct HalfVec<8> {
-  uint4 v;
-  __device__ __forceinline__ uint32_t word(int i) const { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-};
-template <int N>
-__device__ __forceinline__ float half_at(const HalfVec<N> &h, int i) {
-  const uint32_t w = h.word(i >> 1);
-  return __half2float(__ushort_as_half((unsigned short)((i & 1) ? w >> 16 : w & 0xFFFFu)));
+
+// Sixteen bytes into shared memory, past the registers; groups of them complete in order.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+  __syncwarp();
 }
 
 // A piece of a cut item: a run of its slot blocks, begun (off == 0) or ended here or not.
@@ -224,9 +246,24 @@ struct Piece {
   int begins, ends, blocks;   // blocks: thread blocks the whole item reaches (if it begins here)
 };
 
-template <int NT>
+// A warp's block of BS slots in shared memory. Runs of S slots: 64-byte rows, each run 64 bytes
+// (keys) or 16 (values) longer than its rows. A key read takes rows of two runs at once (16 banks
+// apart), a value read rows of four threads' pairs of runs (8 banks apart).
+template <int MT>
+struct alignas(16) Stage {
+  static constexpr int S = 2 * MT, BS = 16 * MT;
+  static constexpr int kKeyRun = S * 64 + 64, kValueRun = S * 64 + 16;
+  uint8_t keys[8 * kKeyRun], values[8 * kValueRun];
+  uint16_t steps[4][BS];  // key scales, key zeros, value scales, value zeros
+};
+
+template <int NT, int MT>
 struct alignas(16) Smem {
   static constexpr int R = 8 * NT;
+  union Block {  // a warp's last piece takes the place of its stage, which is done by then
+    Stage<MT> stage;
+    float tail[R][kPart];
+  } block[kWarps];
   uint2 qfrag[kWarps][NT][8][32];  // B fragments of the queries, by k step and lane
   float qsum[kWarps][R];           // sum of each row's (scaled) query
   float qmul[kWarps][R];           // what the scaling took out
@@ -235,7 +272,6 @@ struct alignas(16) Smem {
   long long before[kThreads], cut[kWarps + 1], base[kWarps];
   int seq[kWarps];
   Piece piece[kWarps][2];
-  alignas(16) float part[kWarps][2][R][kPart];
 };
 
 // x / y and x % y; 32-bit where the counts allow it.
@@ -250,8 +286,15 @@ template <int NT, int MT, bool F32>
 struct Worker {
   static constexpr int R = 8 * NT, BS = 16 * MT, S = 2 * MT;
   const PagedArgs &a;
-  Smem<NT> &sm;
+  Smem<NT, MT> &sm;
   int warp, lane, g, c;
+
+  // Row `row` of piece k (0: of an item begun by an earlier warp, 1: of one begun by this warp) of
+  // a warp: in the workspace, or in the place of the warp's stage.
+  __device__ __forceinline__ float *piece_row(int of_warp, int k, int row) const {
+    return k == 0 ? a.heads + (((int64_t)blockIdx.x * kWarps + of_warp) * R + row) * kPart
+                  : sm.block[of_warp].tail[row];
+  }
 
   // Row tile `rt` of kv head `h` and sequence `s`: rows' queries as B fragments, their sums,
   // scales and positions.
@@ -286,19 +329,20 @@ struct Worker {
       float sum = 0.0f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        // elements (0, 4), (1, 5), (2, 6), (3, 7) of the eight: the pairs of a code word
+        // elements (0, 4), (1, 5), (2, 6), (3, 7) of the eight: the pairs of a code word; the odd
+        // ones meet codes 16 times as large
         const uint32_t x = w[k].x, y = w[k].y, z = w[k].z, v = w[k].w;
         const float e0 = bf16lo(x) * up, e1 = bf16hi(x) * up, e2 = bf16lo(y) * up, e3 = bf16hi(y) * up;
         const float e4 = bf16lo(z) * up, e5 = bf16hi(z) * up, e6 = bf16lo(v) * up, e7 = bf16hi(v) * up;
         sum += ((e0 + e1) + (e2 + e3)) + ((e4 + e5) + (e6 + e7));
-        sm.qfrag[warp][n][2 * k][lane] = make_uint2(pack_f16x2(e0, e4), pack_f16x2(e1, e5));
-        sm.qfrag[warp][n][2 * k + 1][lane] = make_uint2(pack_f16x2(e2, e6), pack_f16x2(e3, e7));
+        sm.qfrag[warp][n][2 * k][lane] = make_uint2(pack_f16x2(e0, e4), pack_f16x2(e1 * 0.0625f, e5 * 0.0625f));
+        sm.qfrag[warp][n][2 * k + 1][lane] = make_uint2(pack_f16x2(e2, e6), pack_f16x2(e3 * 0.0625f, e7 * 0.0625f));
       }
       sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
       sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
       if (c == 0) {
         sm.qsum[warp][8 * n + g] = sum;
-        sm.qmul[warp][8 * n + g] = down * kCode * a.scale_log2;
+        sm.qmul[warp][8 * n + g] = down * kHalfKey * a.scale_log2;
         sm.pos[warp][8 * n + g] = in ? s.len - s.nq + tok : -1;
       }
     }
@@ -327,7 +371,7 @@ struct Worker {
     const int32_t *trow = a.table + (int64_t)b * a.cols;
     const int pmask = (1 << a.page_shift) - 1;
 
-    float o[NT][8][4], own[F32 ? NT : 1][8][4], m[NT][2], l[NT][2], z[NT][2], qm[NT][2];
+    float o[NT][8][4], own[F32 ? NT : 1][8][4], m[NT][2], l[NT][2], z[NT][2], qm[NT][2], qs[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -342,6 +386,7 @@ struct Worker {
         m[n][e] = -INFINITY;
         l[n][e] = z[n][e] = 0.0f;
         qm[n][e] = sm.qmul[warp][8 * n + 2 * c + e];
+        qs[n][e] = sm.qsum[warp][8 * n + 2 * c + e];
       }
     }
 
@@ -355,58 +400,66 @@ struct Worker {
     while (end > i && start_of(end - 1) > last_pos) --end;
     while (i < end && start_of(i) >= a.sinks && a.window > 0 && start_of(i) + BS - 1 <= first_pos - a.window) ++i;
 
-    uint4 kw[S];
-    HalfVec<S> hks, hkz;
-    // a slot without a page reads page 0: the masks below leave it out, and codes are finite
-    auto row_of = [&](int page, int slot) {
-      return (((int64_t)max(page, 0) * a.hkv + h) << a.page_shift) + (slot & pmask);
-    };
-    auto load_keys = [&](int page, int j0) {
-      const int64_t row = row_of(page, j0 + S * g);
-      const uint4 *src = reinterpret_cast<const uint4 *>(a.kc + row * (kD / 2)) + c;
+    // ---- copies of a block: lane q < MT looks up the row (page, head, offset) of the block's q-th
+    // 16 slots. A row index fits 31 bits (the entry point checks).
+    Stage<MT> &st = sm.block[warp].stage;
+    const uint32_t keys_at = tc::smem_u32(st.keys), values_at = tc::smem_u32(st.values);
+    // per 8 slots: 32 lanes x 16 bytes of codes, in one run (S = 8) or two (S = 4)
+    const uint32_t key_lane = S == 8 ? lane * 16u : (lane >> 4) * Stage<MT>::kKeyRun + (lane & 15) * 16u;
+    const uint32_t value_lane = S == 8 ? lane * 16u : (lane >> 4) * Stage<MT>::kValueRun + (lane & 15) * 16u;
+    constexpr uint32_t kKeyStep = S == 8 ? Stage<MT>::kKeyRun : 2 * Stage<MT>::kKeyRun;
+    constexpr uint32_t kValueStep = S == 8 ? Stage<MT>::kValueRun : 2 * Stage<MT>::kValueRun;
+    // steps: 2 MT lanes an array, 8 slots each
+    const int array = lane / (2 * MT), eight = lane % (2 * MT);
+    const __half *step_src = array == 0 ? a.ks : array == 1 ? a.kz : array == 2 ? a.vs : a.vz;
+    const uint32_t step_dst = tc::smem_u32(&st.steps[array & 3][8 * eight]);
+    auto page_at = [&](int k) { return lane < MT ? page_of(trow, start_of(k) + 16 * lane, last_pos) : 0; };
+    // -1: no page; the copies then take page 0, which the masks below leave out
+    auto fetch = [&](int kind, int page, int j0) {
+      const int row = ((max(page, 0) * a.hkv + h) << a.page_shift) + ((j0 + 16 * lane) & pmask);
 #pragma unroll
-      for (int e = 0; e < S; ++e) kw[e] = __ldg(src + 4 * e);
-      hks.v = __ldg(reinterpret_cast<const decltype(hks.v) *>(a.ks + row));
-      hkz.v = __ldg(reinterpret_cast<const decltype(hks.v) *>(a.kz + row));
+      for (int q = 0; q < MT; ++q) {
+        const int64_t at = (int64_t)__shfl_sync(0xFFFFFFFFu, row, q) * (kD / 2) + 16 * lane;
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+          if (kind == 0)
+            copy16(keys_at + key_lane + (2 * q + half) * kKeyStep, a.kc + at + 512 * half);
+          else
+            copy16(values_at + value_lane + (2 * q + half) * kValueStep, a.vc + at + 512 * half);
+      }
+      const int srow = __shfl_sync(0xFFFFFFFFu, row, eight >> 1) + 8 * (eight & 1);
+      if ((array >> 1) == kind) copy16(step_dst, step_src + srow);
+      copy_commit();
     };
-    int page0 = -1, page1 = -1;  // pages of the group's slots in this block and the next
+    int page0 = -1, page1 = -1;  // of this block and the next
     if (i < end) {
-      page0 = page_of(trow, start_of(i) + S * g, last_pos);
-      if (i + 1 < end) page1 = page_of(trow, start_of(i + 1) + S * g, last_pos);
-      load_keys(page0, start_of(i));
+      page0 = page_at(i);
+      if (i + 1 < end) page1 = page_at(i + 1);
+      __syncwarp();
+      fetch(0, page0, start_of(i));
+      fetch(1, page0, start_of(i));
     }
     for (; i < end; ++i) {
       const int j0 = start_of(i);
-      // ---- this block's values and their steps start on their way
-      uint2 vw[2 * S];
-      HalfVec<S> hvs, hvz, vz0, vz1;  // vz0, vz1: zeros of the thread's value slots
-      const int vpage = __shfl_sync(0xFFFFFFFFu, page0, 8 * c);
-      {
-        const int64_t row = row_of(page0, j0 + S * g);
-        hvs.v = __ldg(reinterpret_cast<const decltype(hvs.v) *>(a.vs + row));
-        hvz.v = __ldg(reinterpret_cast<const decltype(hvs.v) *>(a.vz + row));
-      }
-      {
-        const int64_t row = row_of(vpage, j0 + 2 * S * c);
-        const uint2 *src = reinterpret_cast<const uint2 *>(a.vc + row * (kD / 2)) + g;
-#pragma unroll
-        for (int e = 0; e < 2 * S; ++e) vw[e] = __ldg(src + 8 * e);
-        vz0.v = __ldg(reinterpret_cast<const decltype(vz0.v) *>(a.vz + row));
-        vz1.v = __ldg(reinterpret_cast<const decltype(vz0.v) *>(a.vz + row + S));
-      }
+      // the group's slots lie in 16-slot part S g / 16 of the block: has it a page?
+      const bool lost = (__ballot_sync(0xFFFFFFFFu, page0 < 0) >> (S * g / 16)) & 1u;
+      const int page2 = i + 2 < end ? page_at(i + 2) : -1;
+      copy_wait<1>();
+      HalfVec<S> hks, hkz;
+      hks.load(&st.steps[0][S * g]);
+      hkz.load(&st.steps[1][S * g]);
 
       // ---- scores: sc[n][t][..] = (slot of row g: rows 2c, 2c + 1; of row g + 8: the same)
       float sc[NT][MT][4];
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
-        const uint32_t y = zeros_f16(hkz.word(t));
-        const uint32_t zx = __byte_perm(y, y, 0x1010), zy = __byte_perm(y, y, 0x3232);
-        const uint32_t wx[4] = {kw[2 * t].x, kw[2 * t].y, kw[2 * t].z, kw[2 * t].w};
-        const uint32_t wy[4] = {kw[2 * t + 1].x, kw[2 * t + 1].y, kw[2 * t + 1].z, kw[2 * t + 1].w};
+        const uint8_t *key = st.keys + g * Stage<MT>::kKeyRun + 2 * t * 64 + 16 * c;
+        const uint4 kx = *reinterpret_cast<const uint4 *>(key), ky = *reinterpret_cast<const uint4 *>(key + 64);
+        const uint32_t wx[4] = {kx.x, kx.y, kx.z, kx.w}, wy[4] = {ky.x, ky.y, ky.z, ky.w};
 #pragma unroll
         for (int u = 0; u < 8; ++u) {  // k steps of 16 elements
           const uint32_t x = (u & 1) ? wx[u >> 1] >> 8 : wx[u >> 1], v = (u & 1) ? wy[u >> 1] >> 8 : wy[u >> 1];
-          const uint32_t a0 = codes_lo(x, zx), a1 = codes_lo(v, zy), a2 = codes_hi(x, zx), a3 = codes_hi(v, zy);
+          const uint32_t a0 = x & 0x000F000Fu, a1 = v & 0x000F000Fu, a2 = x & 0x00F000F0u, a3 = v & 0x00F000F0u;
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const uint2 qf = sm.qfrag[warp][n][u][lane];
@@ -416,43 +469,46 @@ struct Worker {
         }
       }
 
-      // ---- scores per slot scale (still without the row's factor)
+      // ---- the next block's keys may take this one's place
+      __syncwarp();
+      if (i + 1 < end) {
+        fetch(0, page1, start_of(i + 1));
+        copy_wait<1>();
+      } else {
+        copy_wait<0>();
+      }
+      HalfVec<S> hvs, hvz;
+      hvs.load(&st.steps[2][S * g]);
+      hvz.load(&st.steps[3][S * g]);
+
+      // ---- scores with the slot's scale and zero (still without the row's factor)
       float vsf[S];
-      uint32_t rest = 0u;  // nonzero where a zero is not one of the whole numbers 0 .. 15
+      uint32_t rest = 0u;  // nonzero where a value zero is not one of the whole numbers 0 .. 15
 #pragma unroll
       for (int e = 0; e < S; ++e) {
-        const float kmul = half_at(hks, e);
-        vsf[e] = half_at(hvs, e);
-        if ((e & 1) == 0) rest |= zeros_rest(hkz.word(e >> 1)) | zeros_rest(hvz.word(e >> 1));
+        const float kmul = hks.at(e) * kHalfKey;
+        const float kadd = kmul * hkz.at(e) * (-1.0f / (kHalfKey * kHalfKey));
+        vsf[e] = hvs.at(e);
+        if ((e & 1) == 0) rest |= zeros_rest(hvz.word(e >> 1));
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int r = 0; r < 2; ++r) sc[n][e >> 1][2 * (e & 1) + r] *= kmul;
+          for (int r = 0; r < 2; ++r) {
+            float &x = sc[n][e >> 1][2 * (e & 1) + r];
+            x = fmaf(kadd, qs[n][r], kmul * x);
+          }
       }
       const bool odd = __any_sync(0xFFFFFFFFu, rest != 0u);
-      if (odd) {
-#pragma unroll
-        for (int e = 0; e < S; ++e) {
-          const float kadd = half_at(hks, e) * zero_rest(hkz.word(e >> 1), e & 1) / kCode;
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              float &x = sc[n][e >> 1][2 * (e & 1) + r];
-              x = fmaf(kadd, sm.qsum[warp][8 * n + 2 * c + r], x);
-            }
-        }
-      }
       uint32_t dead = 0u;  // slots that no row sees
       const bool all_seen =
           j0 + BS - 1 <= first_pos && (a.window == 0 || j0 > last_pos - a.window || j0 + BS <= a.sinks);
-      if (__any_sync(0xFFFFFFFFu, !all_seen || page0 < 0)) {
+      if (__any_sync(0xFFFFFFFFu, !all_seen || lost)) {
 #pragma unroll
         for (int e = 0; e < S; ++e) {
           const int j = j0 + S * g + e;
           // a slot no row sees may hold anything, NaN scales too: take it out of the sums
           const bool some =
-              page0 >= 0 && j <= last_pos && (a.window == 0 || j > first_pos - a.window || j < a.sinks);
+              !lost && j <= last_pos && (a.window == 0 || j > first_pos - a.window || j < a.sinks);
           if (!some) {
             vsf[e] = 0.0f;
             dead |= 1u << e;
@@ -467,13 +523,6 @@ struct Worker {
               x = seen ? x : -INFINITY;
             }
         }
-      }
-
-      // ---- the next block's keys, the page after that
-      page0 = page1;
-      if (i + 1 < end) {
-        load_keys(page1, start_of(i + 1));
-        page1 = i + 2 < end ? page_of(trow, start_of(i + 2) + S * g, last_pos) : -1;
       }
 
       // ---- raise the rows' references where a weight could exceed them by too much: the
@@ -521,8 +570,8 @@ struct Worker {
           }
       }
 
-      // ---- weights, two fp16 terms each, in B layout (slots along k)
-      uint32_t ph[NT][S], pl[NT][S];
+      // ---- weights in B layout (slots along k): one fp16 term, for fp32 results two
+      uint32_t ph[NT][S], pl[F32 ? NT : 1][S];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const float m0 = m[n][0] == -INFINITY ? 0.0f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.0f : m[n][1];
@@ -533,22 +582,34 @@ struct Worker {
           const float w0 = p0 * vsf[e], w1 = p1 * vsf[e];
           l[n][0] += p0;
           l[n][1] += p1;
-          if (odd && !(dead >> e & 1u)) {
-            const float vadd = zero_rest(hvz.word(e >> 1), e & 1);
-            z[n][0] = fmaf(w0, vadd, z[n][0]);
-            z[n][1] = fmaf(w1, vadd, z[n][1]);
-          }
           const uint32_t hi = pack_f16x2(w0, w1);
-          const float2 hf = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
           ph[n][e] = movmatrix(hi);
-          pl[n][e] = movmatrix(pack_f16x2(w0 - hf.x, w1 - hf.y));
+          if constexpr (F32) {
+            const float2 hf = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+            pl[n][e] = movmatrix(pack_f16x2(w0 - hf.x, w1 - hf.y));
+          }
+        }
+        if (odd) {
+#pragma unroll
+          for (int e = 0; e < S; ++e) {
+            const float vadd = (dead >> e & 1u) ? 0.0f : vsf[e] * zero_rest(hvz.word(e >> 1), e & 1);
+            z[n][0] = fmaf(ex2(fmaf(sc[n][e >> 1][2 * (e & 1)], qm[n][0], -m0)), vadd, z[n][0]);
+            z[n][1] = fmaf(ex2(fmaf(sc[n][e >> 1][2 * (e & 1) + 1], qm[n][1], -m1)), vadd, z[n][1]);
+          }
         }
       }
 
       // ---- values
+      HalfVec<S> vz0, vz1;  // zeros of the thread's slots
+      vz0.load(&st.steps[3][2 * S * c]);
+      vz1.load(&st.steps[3][2 * S * c + S]);
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
-        const uint2 s0 = vw[2 * t], s1 = vw[S + 2 * t], s2 = vw[2 * t + 1], s3 = vw[S + 2 * t + 1];
+        // slots 2t and 2t + 1 of the thread's two runs
+        const uint8_t *v0 = st.values + 2 * c * Stage<MT>::kValueRun + 2 * t * 64 + 8 * g;
+        const uint8_t *v1 = v0 + Stage<MT>::kValueRun;
+        const uint2 s0 = *reinterpret_cast<const uint2 *>(v0), s1 = *reinterpret_cast<const uint2 *>(v1);
+        const uint2 s2 = *reinterpret_cast<const uint2 *>(v0 + 64), s3 = *reinterpret_cast<const uint2 *>(v1 + 64);
         const uint32_t zx = zeros_f16(__byte_perm(vz0.word(t), vz1.word(t), 0x5410)),
                        zy = zeros_f16(__byte_perm(vz0.word(t), vz1.word(t), 0x7632));
 #pragma unroll
@@ -563,13 +624,17 @@ struct Worker {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               mma_f16(acc[n][2 * q4 + k], a0, a1, a2, a3, ph[n][2 * t], ph[n][2 * t + 1]);
-              mma_f16(acc[n][2 * q4 + k], a0, a1, a2, a3, pl[n][2 * t], pl[n][2 * t + 1]);
+              if constexpr (F32) mma_f16(acc[n][2 * q4 + k], a0, a1, a2, a3, pl[n][2 * t], pl[n][2 * t + 1]);
             }
             x >>= 8;
             y >>= 8;
           }
         }
       }
+      __syncwarp();
+      if (i + 1 < end) fetch(1, page1, start_of(i + 1));
+      page0 = page1;
+      page1 = page2;
       if constexpr (F32) {
         // the tensor cores truncate each sum, so a long chain is a little too small (1.4e-6 of the
         // norm over 870 slots): fp32 results take the chain to a rounded sum every few blocks
@@ -611,12 +676,12 @@ struct Worker {
         if (whole) {
           if (row < rows) store16(s, h, rt * R + row, 16 * g, v);
         } else {
-          float4 *dst = reinterpret_cast<float4 *>(&sm.part[warp][slot][row][16 * g]);
+          float *dst = piece_row(warp, slot, row);
 #pragma unroll
-          for (int t = 0; t < 4; ++t) dst[t] = v[t];
+          for (int t = 0; t < 4; ++t) reinterpret_cast<float4 *>(dst + 16 * g)[t] = v[t];
           if (g == 0) {
-            sm.part[warp][slot][row][kD] = m[n][r];
-            sm.part[warp][slot][row][kD + 1] = l[n][r];
+            dst[kD] = m[n][r];
+            dst[kD + 1] = l[n][r];
           }
         }
       }
@@ -647,11 +712,11 @@ struct Worker {
       const int row = i / (kD / 4), e = 4 * (i % (kD / 4));
       float top = -INFINITY;
       for (int k = first; k <= last; ++k)
-        if (sm.piece[k >> 1][k & 1].rows > 0) top = fmaxf(top, sm.part[k >> 1][k & 1][row][kD]);
+        if (sm.piece[k >> 1][k & 1].rows > 0) top = fmaxf(top, piece_row(k >> 1, k & 1, row)[kD]);
       float den = 0.0f;
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       for (int k = first; k <= last; ++k) {
-        const float *part = sm.part[k >> 1][k & 1][row];
+        const float *part = piece_row(k >> 1, k & 1, row);
         if (sm.piece[k >> 1][k & 1].rows == 0 || part[kD] == -INFINITY) continue;
         const float f = ex2(part[kD] - top);
         const float4 x = *reinterpret_cast<const float4 *>(part + e);
@@ -686,7 +751,7 @@ template <int NT, int MT, bool F32>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k6_paged_attn(const PagedArgs a) {
   constexpr int R = 8 * NT, BS = 16 * MT;
   extern __shared__ float4 smem_raw[];
-  Smem<NT> &sm = *reinterpret_cast<Smem<NT> *>(smem_raw);
+  Smem<NT, MT> &sm = *reinterpret_cast<Smem<NT, MT> *>(smem_raw);
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   tc::grid_dep_launch();
 
@@ -859,7 +924,7 @@ __global__ void __launch_bounds__(R * kD / 4) k6_paged_join(const PagedArgs a) {
 template <int NT, int MT, bool F32>
 cudaError_t launch(PagedArgs a, void *workspace, cudaStream_t stream) {
   constexpr int R = 8 * NT, BS = 16 * MT;
-  constexpr int smem = (int)sizeof(Smem<NT>);
+  constexpr int smem = (int)sizeof(Smem<NT, MT>);
   const void *kern = reinterpret_cast<const void *>(k6_paged_attn<NT, MT, F32>);
   int slots = 0;
   cudaError_t e = resident_slots(kern, kThreads, smem, &slots);
@@ -871,7 +936,8 @@ cudaError_t launch(PagedArgs a, void *workspace, cudaStream_t stream) {
   int64_t grid = slots < kMaxCtas ? slots : kMaxCtas;
   if (most < grid) grid = most;
   a.parts = static_cast<float *>(workspace);
-  a.recs = reinterpret_cast<int4 *>(a.parts + (int64_t)kMaxCtas * 2 * R * kPart);
+  a.heads = a.parts + (int64_t)kMaxCtas * 2 * R * kPart;
+  a.recs = reinterpret_cast<int4 *>(a.heads + (int64_t)kMaxCtas * kWarps * R * kPart);
   k6_paged_attn<NT, MT, F32><<<(unsigned)grid, kThreads, smem, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (blocks < 2 * kSnap || grid == 1) return cudaSuccess;  // no item can reach two blocks
@@ -897,7 +963,7 @@ int rows_per_tile(int group, int max_q_len) {
 
 size_t paged_attention_workspace_bytes(int group, int max_q_len) {
   const size_t r = (size_t)rows_per_tile(group, max_q_len);
-  return (size_t)kMaxCtas * (2 * r * kPart * sizeof(float) + sizeof(int4));
+  return (size_t)kMaxCtas * ((2 + kWarps) * r * kPart * sizeof(float) + sizeof(int4));
 }
 
 cudaError_t launch_paged_attention(const PagedAttention &p, cudaStream_t stream) {
@@ -928,8 +994,8 @@ cudaError_t launch_paged_attention(const PagedAttention &p, cudaStream_t stream)
   a.out = p.out;
   const bool one = rows_per_tile(a.group, p.max_q_len) == 8;
   if (p.out_f32)
-    return one ? launch<1, 2, true>(a, p.workspace, stream) : launch<2, 2, true>(a, p.workspace, stream);
-  return one ? launch<1, 2, false>(a, p.workspace, stream) : launch<2, 2, false>(a, p.workspace, stream);
+    return one ? launch<1, 4, true>(a, p.workspace, stream) : launch<2, 2, true>(a, p.workspace, stream);
+  return one ? launch<1, 4, false>(a, p.workspace, stream) : launch<2, 2, false>(a, p.workspace, stream);
 }
 
 }  // namespace spin

@@ -20,9 +20,9 @@ def random_pages(pages, hkv, page, seed, device="cuda"):
 
 
 def attention(q, cache, table, lens, cu, scale=None, window=0, sinks=0):
-    """(out, magnitude, score magnitude): the result in binary64; per element the sum of
-    p_j s_j (|c_j - 8| + |8 - z_j|), the terms the kernel adds; the largest sum of a score's
-    term sizes. Rows outside the sequences are NaN."""
+    """(out, size, score size, floor): the result in binary64; per element the sum of p_j |vhat_j|,
+    the terms a kernel adds; the largest sum of a score's terms (those of q.c and of z sum(q)); per
+    element max s_j sum |c_j - z_j| of the values. Rows outside the sequences are NaN."""
     q, table = q.double().cpu(), table.cpu()
     cache = {n: t.cpu() for n, t in cache.items()}
     tokens, hq, d = q.shape
@@ -30,7 +30,7 @@ def attention(q, cache, table, lens, cu, scale=None, window=0, sinks=0):
     group = hq // hkv
     scale = 1 / math.sqrt(d) if scale is None else scale
     out = torch.full((tokens, hq, d), math.nan, dtype=torch.float64)
-    size = torch.zeros_like(out)
+    size, floor = torch.zeros_like(out), torch.zeros_like(out)
     score_size = 0.0
     for b, n in enumerate(lens):
         n = min(max(n, 0), table.shape[1] * page)
@@ -63,28 +63,33 @@ def attention(q, cache, table, lens, cu, scale=None, window=0, sinks=0):
                 rows_q = q[t, g * group:(g + 1) * group]
                 w = torch.softmax(rows_q @ k.T * scale, 1)
                 out[t, g * group:(g + 1) * group] = w @ v
-                size[t, g * group:(g + 1) * group] = w @ (((vu[at, g] - 8).abs() + (8 - vz[at, g]).abs()) * vs[at, g])
-                terms = (rows_q.abs() @ (ku[at, g] - 8).abs().T +
-                         rows_q.sum(1).abs()[:, None] * (8 - kz[at, g]).abs().T) * ks[at, g].T * scale
+                size[t, g * group:(g + 1) * group] = w @ v.abs()
+                floor[t, g * group:(g + 1) * group] = vs[at, g].max() * (vu[at, g] - vz[at, g]).abs().sum(0)
+                terms = (rows_q.abs() @ ku[at, g].T + rows_q.sum(1).abs()[:, None] * kz[at, g].T) * ks[at, g].T * scale
                 score_size = max(score_size, float(terms.max()))
-    return out, size, score_size
+    return out, size, score_size, floor
 
 
 def check_attention(got, ref, what=""):
-    """|got - out| <= eps * magnitude (+ half a bf16 step of the value).
+    """|got - out| <= eps * size, and for bf16 results half a step, 2^-8, of the value.
 
-    The weights are two bf16 terms, together within 2^-17 of the fp32 value. A score is a sum of
-    exact products in fp32: at most 128 + 2 additions, each within 2^-23 of the sum of the term
-    sizes S (tensor cores truncate), but the roundings of a tree of 16-wide steps are at most
-    8 + 4 deep: 16 * 2^-23 S covers them. A weight's relative error is that of its score, and
-    enters the numerator and the sum of weights: twice. ex2's 2^-22 and the fp32 sums' few
-    2^-24 steps per block level: 2^-19 together."""
-    out, size, s = ref
+    A score is a sum of exact products in fp32 and its zero's term. The tensor cores add sixteen
+    products at a time and truncate (2^-23 of the size S of the terms each, eight steps); the zero's
+    term, the scale and the row's factor are five roundings of 2^-24: 11 * 2^-23 S at most. A weight
+    is off by that, relatively, and by ex2's 2^-22; both enter the numerator and the sum of weights.
+    For fp32 results a weight is two fp16 terms, 2^-22 of it at most; for bf16 results one, half a
+    step of fp16: 2^-11. The sums: truncated chains of at most 32 products (fp32 results) or of one
+    warp's run (bf16 results; at most 2000 slots here, two terms per 16: 250) of 2^-23 each, and
+    rounded sums of 2^-24 per join: 2^-17 covers both with a value sum of up to 64 such steps, and
+    2^-14 the long chain. A weight's fp16 terms end at steps of 2^-24: with the row's reference such
+    that the largest weight of its block's largest value scale is 2^8 or more, half of that is 2^-33
+    of the largest weight, for each slot: 2^-33 * floor."""
+    out, size, s, floor = ref
     got = got.double().cpu()
     bf16 = what == "bf16"
-    eps = 2 ** -17 + 2 * 16 * 2 ** -23 * s + 2 ** -19
+    eps = 2 * (11 * 2 ** -23 * s + 2 ** -22) + (2 ** -11 + 2 ** -14 if bf16 else 2 ** -22 + 2 ** -17)
     rows = ~torch.isnan(out[:, 0, 0])
-    tol = eps * size + (2 ** -8 * out.abs() if bf16 else 0)
+    tol = eps * size + 2 ** -33 * floor + (2 ** -8 * out.abs() if bf16 else 0)
     bad = ((got - out).abs() > tol + 1e-30)[rows]
     assert torch.isfinite(got[rows]).all()
     assert not bad.any(), f"{int(bad.sum())} elements off, worst {float(((got - out).abs() / (tol + 1e-30))[rows].max()):.3g} x"

@@ -1,8 +1,6 @@
 """Argument rules of the paged INT4 KV cache's entry points that need no GPU: every rejected
 call and every empty one returns before any device access, and the binding refuses host
 tensors, wrong types and shapes."""
-import ctypes as C
-
 import pytest
 import torch
 
@@ -23,13 +21,14 @@ def pages(**kw):
     a = dict(k_cache=FAKE, v_cache=FAKE, k_scale=FAKE, k_zero=FAKE, v_scale=FAKE, v_zero=FAKE, pages=10, n_kv_heads=8,
              page_size=16, head_dim=128)
     a.update(kw)
-    return spin._KvPages(**a)
+    return spin._pack_pages(*(a[n] or 0 for n, _ in spin._KV_ARRAYS), a["pages"], a["n_kv_heads"], a["page_size"],
+                            a["head_dim"])
 
 
 def pool(**kw):
     a = dict(refs=FAKE, free_pages=FAKE, free_count=FAKE)
     a.update(kw)
-    return spin._KvPool(**a)
+    return spin._pack_pool(*(a[n] or 0 for n in ("refs", "free_pages", "free_count")))
 
 
 def attn(L, cache=None, **kw):
@@ -126,4 +125,4 @@ def test_declared_and_exported(L):
     for name in ("spin_paged_attention_int4kv", "spin_paged_attention_workspace_bytes", "spin_kv_pages_copy",
                  "spin_kv_slots_copy", "spin_kv_pages_reserve", "spin_kv_pages_fork", "spin_kv_pages_free"):
         assert name in spin.exported_symbols() and getattr(L, name) is not None
-    assert C.sizeof(spin._KvPages) == 64 and C.sizeof(spin._KvPool) == 24
+    assert len(pages()) == 64 and len(pool()) == 24  # the C structs' sizes
