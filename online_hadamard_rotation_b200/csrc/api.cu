@@ -451,7 +451,9 @@ spin_status_t spin_device_status(uint32_t *status, int reset) {
   if (st == SPIN_OK) st = cuda_status(read_rope_status(&w, reset != 0));
   if (st == SPIN_OK) st = cuda_status(read_dequant_status(&u, reset != 0));
   if (st == SPIN_OK) st = cuda_status(read_gemm_status(&g, reset != 0));
-  *status = v | w | u | g;
+  unsigned int p = 0;
+  if (st == SPIN_OK) st = cuda_status(read_prefill_status(&p, reset != 0));
+  *status = v | w | u | g | p;
   return st;
 }
 

@@ -63,8 +63,10 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cstdint>
 
+#include "paged.cuh"
 #include "spin_launch.h"
 #include "spin_tile.cuh"
 #include "tc_ptx.cuh"
@@ -80,42 +82,10 @@ constexpr int kMaxCtas = 600;  // most blocks of a launch (sets the workspace)
 constexpr int kItem = 2;       // units an item costs besides its slot blocks
 constexpr int kSnap = 3;  // cuts this close to an item's end move there
 constexpr int kMinRun = 4;     // shortest run worth a warp of its own
+constexpr int kNarrowRows = 64;  // rows of a sequence (tokens x group) that are this kernel's in any call
 constexpr int kPart = 132;     // floats per row of a piece: 128 sums, max, sum of weights, pad
 constexpr float kRoom = 9.0f;   // a raised reference leaves weights at most 2^kRoom
 constexpr float kRaise = 5.0f;  // log2 above that at which it is raised again (fp16 ends at 2^16)
-
-struct PagedArgs {
-  const __nv_bfloat16 *q;
-  const uint8_t *kc, *vc;
-  const __half *ks, *kz, *vs, *vz;
-  const int32_t *table, *lens, *cu;
-  int tokens, seqs, cols, num_pages, page_shift, cap;  // cap: slots a table row can name
-  int hq, hkv, group, window, sinks;
-  float scale_log2;  // softmax scale x log2(e)
-  void *out;
-  float *parts;  // [grid][2][R][kPart]
-  float *heads;  // [grid][kWarps][R][kPart], read by the block that wrote them
-  int4 *recs;    // [grid]
-};
-
-struct Seq {
-  int len, q0, nq;
-};
-
-// Lengths and offsets outside their ranges are clamped: no index derived from them can
-// leave the buffers.
-__device__ __forceinline__ Seq load_seq(const PagedArgs &a, int b) {
-  Seq s;
-  s.len = min(max(a.lens[b], 0), a.cap);
-  if (a.cu == nullptr) {
-    s.q0 = b;
-    s.nq = 1;
-  } else {
-    s.q0 = min(max(a.cu[b], 0), a.tokens);
-    s.nq = min(max(a.cu[b + 1], s.q0), a.tokens) - s.q0;
-  }
-  return s;
-}
 
 // The slot blocks of a sequence: nsink blocks from slot 0, then blocks first .. end - 1.
 struct Blocks {
@@ -134,13 +104,8 @@ __device__ __forceinline__ Blocks seq_blocks(const PagedArgs &a, const Seq &s) {
 
 template <int R>
 __device__ __forceinline__ int row_tiles(const PagedArgs &a, const Seq &s) {
-  return (s.nq * a.group + R - 1) / R;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
+  const int rows = s.nq * a.group;
+  return rows > a.row_limit ? 0 : (rows + R - 1) / R;
 }
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
@@ -176,12 +141,6 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t x, uint32_t y) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
   return r;
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 __device__ __forceinline__ uint32_t fma_f16x2(uint32_t x, uint32_t y, uint32_t z) {
   uint32_t r;
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(z));
@@ -993,6 +952,15 @@ cudaError_t launch_paged_attention(const PagedAttention &p, cudaStream_t stream)
   a.scale_log2 = p.softmax_scale * 1.4426950408889634f;
   a.out = p.out;
   const bool one = rows_per_tile(a.group, p.max_q_len) == 8;
+  a.row_limit = INT_MAX;
+  // chunks of prompts go to the tensor-memory kernel, other sequences of the same call (if there
+  // can be any) stay here; fp32 results do too, whose weights want two terms
+  if (!p.out_f32 && (int64_t)p.max_q_len * a.group > kNarrowRows &&
+      paged_prefill_worth(a.tokens, a.group, a.hkv)) {
+    a.row_limit = kNarrowRows;
+    const cudaError_t e = launch_paged_prefill(a, stream);
+    if (e != cudaSuccess) return e;
+  }
   if (p.out_f32)
     return one ? launch<1, 4, true>(a, p.workspace, stream) : launch<2, 2, true>(a, p.workspace, stream);
   return one ? launch<1, 4, false>(a, p.workspace, stream) : launch<2, 2, false>(a, p.workspace, stream);

@@ -223,16 +223,26 @@ __device__ __forceinline__ int stack_page(const PoolArgs &a, int count, long lon
 
 __device__ __forceinline__ int free_pages_of(const PoolArgs &a) { return min(max(*a.count, 0), a.pages); }
 
-// One block: the pages wanted by each row, a prefix sum, then each served row's columns.
+constexpr int kOwnWant = 4;  // a row that wants more pages than this is filled by a warp
+
+// One block: the pages wanted by each row, a prefix sum, then each served row's columns. A decode
+// step wants at most a page or two a row, which its thread writes itself; the long rows of a
+// prompt are left to whole warps (with warps for every row, 1280 rows took 30 us).
 __global__ void __launch_bounds__(kPlanThreads)
     k7_reserve(const PoolArgs a, const int32_t *__restrict__ add, int32_t *__restrict__ status) {
   __shared__ long long sums[kPlanThreads / 32];
+  __shared__ unsigned long long s_taken;
+  __shared__ int s_long[kPlanThreads], s_longs;
   __shared__ long long s_depth[kPlanThreads];
   __shared__ int s_want[kPlanThreads], s_have[kPlanThreads];
-  const int count = free_pages_of(a);
-  long long carry = 0, taken = 0;
+  const int count = free_pages_of(a), t = threadIdx.x;
+  if (t == 0) {
+    s_taken = 0;
+    s_longs = 0;
+  }
+  long long carry = 0;
   for (int b0 = 0; b0 < a.rows; b0 += kPlanThreads) {
-    const int b = b0 + threadIdx.x;
+    const int b = b0 + t;
     long long want = 0, have = 0;
     int st = SPIN_KV_REFUSED, len = 0, n = 0;
     if (b < a.rows) {
@@ -247,6 +257,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
     long long total;
     const long long upto = carry + block_scan(want, sums, total);
+    carry += total;
     if (want > 0 && upto > count) {
       st = SPIN_KV_NO_PAGES;
       want = 0;
@@ -255,31 +266,33 @@ __global__ void __launch_bounds__(kPlanThreads)
       status[b] = st;
       if (st == SPIN_KV_OK) a.lens[b] = len + n;
     }
-    s_depth[threadIdx.x] = upto - want;
-    s_want[threadIdx.x] = (int)want;
-    s_have[threadIdx.x] = (int)have;
-    // a served row's want is the last part of its prefix, so the largest one is what was taken
-    const int any = __syncthreads_or(want > 0);
-    if (any) {
-      const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-      for (int r = warp; r < kPlanThreads; r += kPlanThreads / 32) {
-        const int w = s_want[r];
-        for (int j = lane; j < w; j += 32) {
-          const int id = stack_page(a, count, s_depth[r] + j);
-          a.table[(int64_t)(b0 + r) * a.cols + s_have[r] + j] = id;
-          if (id >= 0) a.refs[id] = 1;
-        }
+    auto give = [&](int64_t row, int col, long long depth) {
+      const int id = stack_page(a, count, depth);
+      a.table[row * a.cols + col] = id;
+      if (id >= 0) a.refs[id] = 1;
+    };
+    if (want > 0) {
+      // served rows are the first of the prefix, so the largest one is what was taken
+      atomicMax(&s_taken, (unsigned long long)upto);
+      if (want <= kOwnWant) {
+        for (int j = 0; j < (int)want; ++j) give(b, (int)have + j, upto - want + j);
+      } else {
+        const int k = atomicAdd(&s_longs, 1);  // any order: each row's pages are fixed
+        s_long[k] = b;
+        s_depth[k] = upto - want;
+        s_want[k] = (int)want;
+        s_have[k] = (int)have;
       }
-      for (int x = kPlanThreads - 1; x >= 0; --x)
-        if (s_want[x] > 0) {
-          taken = s_depth[x] + s_want[x];
-          break;
-        }
-      __syncthreads();
     }
-    carry += total;
+    __syncthreads();
+    const int longs = s_longs;
+    for (int k = t >> 5; k < longs; k += kPlanThreads / 32)
+      for (int j = t & 31; j < s_want[k]; j += 32) give(s_long[k], s_have[k] + j, s_depth[k] + j);
+    __syncthreads();
+    if (t == 0) s_longs = 0;
   }
-  if (threadIdx.x == 0 && taken > 0) *a.count = count - (int)taken;
+  __syncthreads();
+  if (t == 0 && s_taken > 0) *a.count = count - (int)s_taken;
 }
 
 // Fork, first step (one block): lengths of the parents as they are before any fork, claims of

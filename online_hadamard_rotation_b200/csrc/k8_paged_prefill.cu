@@ -1,0 +1,568 @@
+// k8_paged_prefill.cu -- attention of many new tokens per sequence over the paged INT4 KV cache,
+// on the 5th-generation tensor cores.
+//
+// The operator of k6_paged_attn.cu (formulas, masks and row order there) for sequences with more
+// (token, query head) rows than its narrow tiles are good for: chunks of a prompt. It is bound by
+// arithmetic: 4 x 128 flops per row and visible slot on the tensor cores, and one exponential each
+// on the special-function units (16 a cycle and SM, twice the time of the products).
+//
+// A block of threads takes 256 rows of one kv head (64 tokens at 4 query heads per kv head) and
+// walks the visible slots 128 at a time. The codes are expanded once for all 256 rows:
+//   keys    (c - z) s 2^-e in fp16, e the exponent above the tile's largest s (one rounding, 2^-12)
+//   values  (c - z) 2^-9, exact for whole zeros; their scales go into the weights
+// as K-major and MN-major operands with the 128-byte swizzle (eight codes of a word come out in
+// the order 0, 4, 1, 5, 2, 6, 3, 7; the queries are packed alike and the output is put back).
+// Queries are scaled by a power of two per row, as in k6, so they are exact in fp16.
+//   warps 0-3, 4-7  softmax of rows 0-127 and 128-255: a thread owns a row (a TMEM lane), reads its
+//                   scores, writes the weights p s' as fp16 over them (the A operand of the value
+//                   product stays in TMEM), and rescales its sums only when its reference moves
+//   warps 8-11      converters: thread = slot, the next two tiles' codes already in registers
+//   warp 12         issues the products: S_w = Q_w K^T and O_w += P_w V for w = 0, 1 in turn, so that
+//                   one half's products run under the other half's exponentials
+// TMEM: S_0, S_1, O_0, O_1 of 128 columns each, all 512.
+// Every wait is bounded by a clock budget; on expiry the block records a status (read by
+// spin_device_status), stops, waits for its products and frees TMEM.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "paged.cuh"
+#include "spin_launch.h"
+#include "spin_tile.cuh"
+#include "tc_ptx.cuh"
+
+namespace spin {
+
+// Nonzero once a paged prefill launch gave up on a wait (see spin_device_status).
+__device__ unsigned int g_prefill_status = 0u;
+
+namespace {
+
+constexpr int kD = 128;
+constexpr int kThreads = 13 * 32;
+constexpr int kRows = 256;      // rows of a block of threads, two halves of 128
+constexpr int kTile = 128;      // slots of a tile
+constexpr uint32_t kOperand = kTile * kD * 2;  // bytes of a 128 x 128 fp16 operand
+constexpr uint32_t kOffQ = 0, kOffK = 2 * kOperand, kOffV = 4 * kOperand, kOffS = 6 * kOperand;
+constexpr float kRoom = 9.0f;   // a raised reference leaves weights at most 2^kRoom
+constexpr float kRaise = 5.0f;  // log2 above that at which it is raised again (fp16 ends at 2^16)
+constexpr float kCode = 512.0f; // what the value codes' 2^-9 takes out
+constexpr long long kTimeoutCycles = 4000000000LL;  // about two seconds
+
+struct Shared {
+  uint64_t qfull, kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], pvdone[2], drain;
+  uint32_t tmem_base;
+  int abort;
+  int seq, pair;               // the block's item
+  int sums[kThreads / 32], total;
+  alignas(16) float vs[2][kTile];  // value scales of a stage's slots (0 for those no row sees)
+  float kscale[2], vexp[2];    // 2^e of the keys; exponent above the largest value scale
+  uint32_t seen[2][4];         // slots of the stage that have a page and lie before the last row
+  uint32_t kmax[4], vmax[4];   // converters' warps
+};
+constexpr uint32_t kSmemBytes = kOffS + sizeof(Shared) + 1024;  // + alignment slack
+static_assert(kSmemBytes <= 232448, "shared memory per block");
+
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Shared &S, bool honor_abort = true) {
+  if (tc::mbar_try_wait_suspend(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (tc::mbar_try_wait_suspend(bar, parity)) return true;
+    if (honor_abort && *reinterpret_cast<volatile int *>(&S.abort)) return false;
+    if (clock64() - t0 > kTimeoutCycles) {
+      *reinterpret_cast<volatile int *>(&S.abort) = 1;
+      atomicOr(&g_prefill_status, 1u);
+      return false;
+    }
+  }
+}
+// The same for a warp whose lanes go on together.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Shared &S) {
+  return __all_sync(0xFFFFFFFFu, wait(bar, parity, S));
+}
+
+// kind::f16 with fp16 operands, fp32 sums, M = N = 128; B K-major or MN-major.
+constexpr uint32_t idesc(bool b_mn) {
+  return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+// D[tmem] (+)= A[tmem] B[smem]: A is fp16, lane = row, two elements a column.
+__device__ __forceinline__ void umma_tmem_a(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(id), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t x, uint32_t y, uint32_t z) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(z));
+  return r;
+}
+__device__ __forceinline__ uint32_t twice(__half h) {
+  const uint32_t b = __half_as_ushort(h);
+  return b | (b << 16);
+}
+
+// Eight codes as (u - z) 2^-9, from zero = -z 2^-9: a nibble under a mask is the subnormal u 2^-24
+// or u 2^-20.
+__device__ __forceinline__ uint4 codes8(uint32_t w, uint32_t zero) {
+  const uint32_t v = w >> 8;
+  return make_uint4(
+      fma_f16x2(w & 0x000F000Fu, 0x78007800u, zero), fma_f16x2(w & 0x00F000F0u, 0x68006800u, zero),
+      fma_f16x2(v & 0x000F000Fu, 0x78007800u, zero), fma_f16x2(v & 0x00F000F0u, 0x68006800u, zero));
+}
+
+// Byte offset of 16-byte piece j (eight elements) of row r of an operand: two atoms of 64 elements,
+// rows of 128 bytes, 128-byte swizzle.
+__device__ __forceinline__ uint32_t piece_at(uint32_t r, uint32_t j) {
+  return (j >> 3) * (kTile * 128u) + r * 128u + (((j & 7u) ^ (r & 7u)) << 4);
+}
+
+struct Slot {  // what a converter holds of its slot of a tile
+  uint4 k[4], v[4];
+  __half ks, kz, vs, vz;
+  bool has;  // a page, and a row that may see it
+};
+
+__global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+  Shared &S = *reinterpret_cast<Shared *>(smem + kOffS);
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+
+  // ---- the block's item: 256-row pairs of tiles of the sequences above the row limit, the last
+  // (longest) of a sequence first, heads innermost
+  const int want = blockIdx.x / a.hkv, h = blockIdx.x - want * a.hkv;
+  {
+    const int per = (a.seqs + kThreads - 1) / kThreads;
+    const int b0 = min(t * per, a.seqs), b1 = min(b0 + per, a.seqs);
+    auto pairs = [&](int b) {
+      const Seq s = load_seq(a, b);
+      const int rows = s.nq * a.group;
+      return rows > a.row_limit ? (rows + kRows - 1) / kRows : 0;
+    };
+    int mine = 0;
+    for (int b = b0; b < b1; ++b) mine += pairs(b);
+    int upto = mine;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, upto, x);
+      if (lane >= x) upto += v;
+    }
+    if (lane == 31) S.sums[warp] = upto;
+    if (t == 0) S.seq = -1;
+    __syncthreads();
+    int before = upto - mine;
+    for (int w = 0; w < warp; ++w) before += S.sums[w];
+    if (want >= before && want < before + mine)
+      for (int b = b0; b < b1; ++b) {
+        const int n = pairs(b);
+        if (want < before + n) {
+          S.seq = b;
+          S.pair = n - 1 - (want - before);
+          break;
+        }
+        before += n;
+      }
+    __syncthreads();
+  }
+  const int b = S.seq;
+  if (b < 0) return;
+  const Seq s = load_seq(a, b);
+  const int rr0 = S.pair * kRows, rows = min(kRows, s.nq * a.group - rr0);
+  const int halves = rows > 128 ? 2 : 1;
+  const int first_pos = s.len - s.nq + rr0 / a.group, last_pos = s.len - s.nq + (rr0 + rows - 1) / a.group;
+  // tiles: nsink from slot 0, then first ..
+  const int end = last_pos / kTile + (last_pos >= 0 ? 1 : 0);
+  const int oldest = a.window > 0 ? max(0, first_pos - a.window + 1) : 0;
+  const int first = min(oldest / kTile, end);
+  const int nsink = a.window > 0 ? min((min(a.sinks, last_pos + 1) + kTile - 1) / kTile, first) : 0;
+  const int tiles = last_pos < 0 ? 0 : max(nsink, 0) + end - first;
+  auto start_of = [&](int i) { return (i < nsink ? i : i - nsink + first) * kTile; };
+
+  // ---- setup
+  if (t == 0) {
+    tc::mbar_init(&S.qfull, 256);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&S.kfull[i], 128);
+      tc::mbar_init(&S.vfull[i], 128);
+      tc::mbar_init(&S.kempty[i], 1);
+      tc::mbar_init(&S.vempty[i], 1);
+      tc::mbar_init(&S.sfull[i], 1);
+      tc::mbar_init(&S.pfull[i], 128);
+      tc::mbar_init(&S.pvdone[i], 1);
+    }
+    tc::mbar_init(&S.drain, 1);
+    S.abort = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == 12) {
+    tc::tmem_alloc(&S.tmem_base, 512);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+
+  if (warp < 8) {
+    // ================================================================ softmax: half w, thread = row
+    const int w = warp >> 2, r = t & 127;
+    const int rr = rr0 + 128 * w + r;
+    const bool in = 128 * w + r < rows;
+    const int tok = rr / a.group;
+    const int64_t qrow = ((int64_t)(s.q0 + tok) * a.hq + h * a.group + (rr - tok * a.group)) * kD;
+    const int pos = in ? s.len - s.nq + tok : -1;
+    // the half's positions, for tiles that all of its rows see
+    const int lo_pos = s.len - s.nq + (rr0 + 128 * w) / a.group;
+    const int hi_pos = s.len - s.nq + (rr0 + min(128 * w + 127, rows - 1)) / a.group;
+    const uint32_t s_at = tmem + 128u * w + ((uint32_t)(warp & 3) << 21);        // lane quarter in bits 16+
+    const uint32_t o_at = tmem + 256u + 128u * w + ((uint32_t)(warp & 3) << 21);
+    float qmul;
+    {
+      // the row's largest exponent, then its values times 2^(14 - e) in fp16
+      const uint4 *src = reinterpret_cast<const uint4 *>(a.q + qrow);
+      uint32_t top = 0u;
+#pragma unroll 4
+      for (int j = 0; j < 16; ++j) {
+        const uint4 x = in ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top = max(top, max(v[k] & 0x7FFFu, (v[k] >> 16) & 0x7FFFu));
+      }
+      const int e = min(max((int)(top >> 7) - 127, -100), 126);
+      const float up = __int_as_float((min(14 - e, 126) + 127) << 23);
+      qmul = __int_as_float((127 - min(14 - e, 126)) << 23) * a.scale_log2;
+      uint8_t *qs = smem + kOffQ + w * kOperand;
+#pragma unroll 4
+      for (int j = 0; j < 16; ++j) {
+        const uint4 x = in ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4 *>(qs + piece_at(r, j)) = make_uint4(
+            pack_f16x2(bf16lo(x.x) * up, bf16lo(x.z) * up), pack_f16x2(bf16hi(x.x) * up, bf16hi(x.z) * up),
+            pack_f16x2(bf16lo(x.y) * up, bf16lo(x.w) * up), pack_f16x2(bf16hi(x.y) * up, bf16hi(x.w) * up));
+      }
+      tc::fence_proxy_async_smem();
+      tc::mbar_arrive(&S.qfull);
+    }
+    float m = -INFINITY, l = 0.0f;
+    bool ok = w < halves;
+    for (int i = 0; ok && i < tiles; ++i) {
+      const int st = i & 1;
+      const uint32_t ph = (uint32_t)(i >> 1) & 1u;
+      if (!(ok = wait_warp(&S.sfull[w], (uint32_t)i & 1u, S))) break;
+      if (!(ok = wait_warp(&S.vfull[st], ph, S))) break;
+      tc::tc_fence_after();
+      const int j0 = start_of(i);
+      const float f = qmul * S.kscale[st];
+      const float vexp = S.vexp[st];
+      const uint32_t seen[4] = {S.seen[st][0], S.seen[st][1], S.seen[st][2], S.seen[st][3]};
+      const bool all_seen = (seen[0] & seen[1] & seen[2] & seen[3]) == 0xFFFFFFFFu && j0 + kTile - 1 <= lo_pos &&
+                            (a.window == 0 || j0 > hi_pos - a.window || j0 + kTile <= a.sinks);
+      // slots of 32-slot part c that this row sees, as bits
+      auto visible = [&](int c) -> uint32_t {
+        const int j = j0 + 32 * c;
+        auto below = [&](int n) -> uint32_t {  // slots before n
+          const int k = n - j;
+          return k <= 0 ? 0u : k >= 32 ? 0xFFFFFFFFu : (1u << k) - 1u;
+        };
+        uint32_t v = below(pos + 1);
+        if (a.window > 0) v &= ~below(pos - a.window + 1) | below(a.sinks);
+        return v & seen[c];
+      };
+      // ---- the row's largest score
+      float top = -INFINITY;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t x[32];
+        tc::tmem_ld32(s_at + 32u * c, x);
+        tc::tmem_wait_ld();
+        if (all_seen) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 2)
+            top = fmaxf(top, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
+        } else {
+          const uint32_t v = visible(c);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) top = fmaxf(top, (v >> k & 1u) ? __uint_as_float(x[k]) : -INFINITY);
+        }
+      }
+      top = fmaf(top, f, vexp);
+      // ---- raise the reference where a weight could exceed it by too much
+      const bool raise = top > m + kRoom + kRaise;  // false while both are -inf
+      if (__any_sync(0xFFFFFFFFu, raise)) {
+        const float mn = raise ? top - kRoom : m;
+        const float fac = raise ? ex2(m - mn) : 1.0f;
+        m = mn;
+        l *= fac;
+        if (i > 0) {
+          // the products of the tile before have been added
+          if (!(ok = wait_warp(&S.pvdone[w], (uint32_t)(i - 1) & 1u, S))) break;
+          tc::tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t x[16];
+            tmem_ld16(o_at + 16u * c, x);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * fac);
+            tmem_st16(o_at + 16u * c, x);
+          }
+          tmem_wait_st();
+        }
+      }
+      // ---- weights over the scores: 32 scores become 16 columns that lie before them
+      const float mr = m == -INFINITY ? 0.0f : m;
+      float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t x[32], p[16];
+        tc::tmem_ld32(s_at + 32u * c, x);
+        const float4 *vs = reinterpret_cast<const float4 *>(&S.vs[st][32 * c]);
+        tc::tmem_wait_ld();
+        if (!all_seen) {
+          const uint32_t v = visible(c);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] = (v >> k & 1u) ? x[k] : 0xFF800000u;
+        }
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+          const float4 s4 = vs[k >> 2];
+          const float2 y0 = fma2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), f, -mr);
+          const float2 y1 = fma2(make_float2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])), f, -mr);
+          const float p0 = ex2(y0.x), p1 = ex2(y0.y), p2 = ex2(y1.x), p3 = ex2(y1.y);
+          l0 += p0 + p2;
+          l1 += p1 + p3;
+          p[k >> 1] = pack_f16x2(p0 * s4.x, p1 * s4.y);
+          p[(k >> 1) + 1] = pack_f16x2(p2 * s4.z, p3 * s4.w);
+        }
+        tmem_st16(s_at + 16u * c, p);
+      }
+      l += l0 + l1;
+      tmem_wait_st();
+      tc::tc_fence_before();
+      tc::mbar_arrive(&S.pfull[w]);
+    }
+    // ---- result
+    if (ok && tiles > 0) ok = wait_warp(&S.pvdone[w], (uint32_t)(tiles - 1) & 1u, S);
+    if (w < halves && ok) {
+      tc::tc_fence_after();
+      const float inv = l > 0.0f ? kCode / l : 0.0f;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t x[32];
+        if (tiles > 0) {
+          tc::tmem_ld32(o_at + 32u * c, x);
+          tc::tmem_wait_ld();
+        }
+        if (!in) continue;
+        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + qrow + 32 * c);
+#pragma unroll
+        for (int k = 0; k < 32; k += 8) {
+          auto v = [&](int e) { return m == -INFINITY ? 0.0f : __uint_as_float(x[k + e]) * inv; };
+          dst[k >> 3] = make_uint4(pack_bf16x2(v(0), v(2)), pack_bf16x2(v(4), v(6)), pack_bf16x2(v(1), v(3)),
+                                   pack_bf16x2(v(5), v(7)));
+        }
+      }
+    }
+  } else if (warp < 12) {
+    // ================================================================ converters: thread = slot
+    const int c = t - 256, cw = warp - 8;
+    const int32_t *trow = a.table + (int64_t)b * a.cols;
+    const int pmask = (1 << a.page_shift) - 1;
+    auto load = [&](int i, Slot &x) {
+      if (i >= tiles) return;
+      const int j = start_of(i) + c;
+      int id = -1;
+      if (j <= last_pos) {
+        id = __ldg(trow + (j >> a.page_shift));
+        if ((unsigned)id >= (unsigned)a.num_pages) id = -1;
+      }
+      // a slot that no row sees may hold anything: keep it out
+      x.has = id >= 0 && (a.window == 0 || j > first_pos - a.window || j < a.sinks);
+      if (!x.has) id = 0;
+      const int64_t row = (((int64_t)id * a.hkv + h) << a.page_shift) + (j & pmask);
+      const uint4 *k = reinterpret_cast<const uint4 *>(a.kc + row * (kD / 2));
+      const uint4 *v = reinterpret_cast<const uint4 *>(a.vc + row * (kD / 2));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        x.k[q] = __ldg(k + q);
+        x.v[q] = __ldg(v + q);
+      }
+      x.ks = a.ks[row];
+      x.kz = a.kz[row];
+      x.vs = a.vs[row];
+      x.vz = a.vz[row];
+    };
+    const __half zero = __float2half_rn(0.0f);
+    auto convert = [&](int i, const Slot &x) -> bool {
+      const int st = i & 1;
+      const uint32_t ph = (uint32_t)(i >> 1) & 1u;
+      // exponents above the tile's largest scales
+      const float ks = x.has ? __half2float(x.ks) : 0.0f, vs = x.has ? __half2float(x.vs) : 0.0f;
+      const uint32_t kb = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(ks)));
+      const uint32_t vb = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(vs)));
+      const uint32_t has = __ballot_sync(0xFFFFFFFFu, x.has);
+      tc::named_sync(1, 128);  // the tile before has read kmax and vmax
+      if (lane == 0) {
+        S.kmax[cw] = kb;
+        S.vmax[cw] = vb;
+      }
+      tc::named_sync(1, 128);
+      const uint32_t kt = max(max(S.kmax[0], S.kmax[1]), max(S.kmax[2], S.kmax[3]));
+      const uint32_t vt = max(max(S.vmax[0], S.vmax[1]), max(S.vmax[2], S.vmax[3]));
+      const int ke = max((int)(kt >> 23) - 126, -24), ve = max((int)(vt >> 23) - 126, -24);
+      if (i >= 2 && !wait_warp(&S.kempty[st], ph ^ 1u, S)) return false;
+      {
+        const uint32_t z = twice(x.has ? __float2half_rn(__half2float(x.kz) * (-1.0f / 512.0f)) : zero);
+        const uint32_t mul = twice(__float2half_rn(ks * __int_as_float((127 + 9 - ke) << 23)));
+        uint8_t *dst = smem + kOffK + st * kOperand;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t word[4] = {x.k[q].x, x.k[q].y, x.k[q].z, x.k[q].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint4 y = codes8(word[e], z);
+            *reinterpret_cast<uint4 *>(dst + piece_at(c, 4 * q + e)) =
+                make_uint4(mul_f16x2(y.x, mul), mul_f16x2(y.y, mul), mul_f16x2(y.z, mul), mul_f16x2(y.w, mul));
+          }
+        }
+        tc::fence_proxy_async_smem();
+        tc::mbar_arrive(&S.kfull[st]);
+      }
+      if (i >= 2 && !wait_warp(&S.vempty[st], ph ^ 1u, S)) return false;
+      {
+        const uint32_t z = twice(x.has ? __float2half_rn(__half2float(x.vz) * (-1.0f / 512.0f)) : zero);
+        uint8_t *dst = smem + kOffV + st * kOperand;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t word[4] = {x.v[q].x, x.v[q].y, x.v[q].z, x.v[q].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4 *>(dst + piece_at(c, 4 * q + e)) = codes8(word[e], z);
+        }
+        S.vs[st][c] = vs;
+        if (lane == 0) S.seen[st][cw] = has;
+        if (c == 0) {
+          S.kscale[st] = __int_as_float((127 + ke) << 23);
+          S.vexp[st] = (float)ve;
+        }
+        tc::fence_proxy_async_smem();
+        tc::mbar_arrive(&S.vfull[st]);
+      }
+      return true;
+    };
+    Slot even, odd;
+    load(0, even);
+    load(1, odd);
+    for (int i = 0; i < tiles; i += 2) {
+      if (!convert(i, even)) break;
+      load(i + 2, even);
+      if (i + 1 >= tiles || !convert(i + 1, odd)) break;
+      load(i + 3, odd);
+    }
+  } else if (lane == 0 && tiles > 0) {
+    // ================================================================ products
+    const uint32_t sQ = tc::smem_u32(smem + kOffQ), sK = tc::smem_u32(smem + kOffK), sV = tc::smem_u32(smem + kOffV);
+    auto scores = [&](int w, int st) {  // S_w = Q_w K^T
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t at = (uint32_t)(k >> 2) * (kTile * 128u) + (uint32_t)(k & 3) * 32u;
+        tc::umma_bf16(tmem + 128u * w, tc::smem_desc(sQ + w * kOperand + at, 16, 1024),
+                      tc::smem_desc(sK + st * kOperand + at, 16, 1024), idesc(false), k > 0 ? 1u : 0u);
+      }
+      tc::umma_commit(&S.sfull[w]);
+    };
+    bool ok = wait(&S.qfull, 0, S) && wait(&S.kfull[0], 0, S);
+    if (ok) {
+      tc::tc_fence_after();
+      for (int w = 0; w < halves; ++w) scores(w, 0);
+      tc::umma_commit(&S.kempty[0]);
+    }
+    for (int i = 0; ok && i < tiles; ++i) {
+      const int st = i & 1;
+      const uint32_t ph = (uint32_t)(i >> 1) & 1u;
+      for (int w = 0; ok && w < halves; ++w) {
+        ok = wait(&S.vfull[st], ph, S) && wait(&S.pfull[w], (uint32_t)i & 1u, S);
+        if (!ok) break;
+        tc::tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)  // O_w += P_w V, 16 slots a step
+          umma_tmem_a(tmem + 256u + 128u * w, tmem + 128u * w + 8u * k,
+                      tc::smem_desc(sV + st * kOperand + (uint32_t)k * 16u * 128u, kTile * 128u, 1024), idesc(true),
+                      (i > 0 || k > 0) ? 1u : 0u);
+        tc::umma_commit(&S.pvdone[w]);
+        if (w == halves - 1) tc::umma_commit(&S.vempty[st]);
+        if (i + 1 < tiles) {
+          const int sn = (i + 1) & 1;
+          // the next scores take the place of the weights that are being read
+          ok = wait(&S.kfull[sn], (uint32_t)((i + 1) >> 1) & 1u, S) && wait(&S.pvdone[w], (uint32_t)i & 1u, S);
+          if (!ok) break;
+          tc::tc_fence_after();
+          scores(w, sn);
+          if (w == halves - 1) tc::umma_commit(&S.kempty[sn]);
+        }
+      }
+    }
+  }
+
+  // ---- teardown
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    if (lane == 0) {
+      tc::umma_commit(&S.drain);  // arrives once every product this thread issued is complete
+      wait(&S.drain, 0, S, false);
+    }
+    __syncwarp();
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace
+
+bool paged_prefill_worth(int tokens, int group, int n_kv_heads) {
+  // below half a block per SM the finer cuts of the narrow kernel fill the GPU better
+  return (int64_t)n_kv_heads * tokens * group / kRows >= 74;
+}
+
+cudaError_t launch_paged_prefill(const PagedArgs &a, cudaStream_t stream) {
+  const void *kern = reinterpret_cast<const void *>(k8_paged_prefill);
+  int slots = 0;
+  const cudaError_t e = resident_slots(kern, kThreads, (int)kSmemBytes, &slots);
+  if (e != cudaSuccess) return e;
+  // sequences above the limit have at least row_limit + 1 rows
+  const int64_t rows = (int64_t)a.tokens * a.group;
+  const int64_t most = rows / (a.row_limit + 1) < a.seqs ? rows / (a.row_limit + 1) : a.seqs;
+  const int64_t grid = (rows / kRows + most) * a.hkv;
+  if (grid <= 0) return cudaSuccess;
+  k8_paged_prefill<<<(unsigned)grid, kThreads, kSmemBytes, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t read_prefill_status(unsigned int *status, bool reset) {
+  cudaError_t e = cudaMemcpyFromSymbol(status, g_prefill_status, sizeof(unsigned int));
+  if (e != cudaSuccess || !reset) return e;
+  const unsigned int zero = 0u;
+  return cudaMemcpyToSymbol(g_prefill_status, &zero, sizeof(unsigned int));
+}
+
+}  // namespace spin

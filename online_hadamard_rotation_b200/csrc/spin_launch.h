@@ -85,6 +85,7 @@ struct PagedAttention {
 };
 size_t paged_attention_workspace_bytes(int group, int max_q_len);
 cudaError_t launch_paged_attention(const PagedAttention &p, cudaStream_t stream);
+cudaError_t read_prefill_status(unsigned int *status, bool reset);  // k8_paged_prefill.cu
 // W4A4 GEMM on packed INT4 codes (k5_w4a4_gemm.cu): shapes it takes (n_out a multiple
 // of 256, k a multiple of 128 up to 65536), the launch, and its status word.
 bool w4a4_shape_supported(int64_t tokens, int n_out, int k);

@@ -20,7 +20,7 @@ def random_pages(pages, hkv, page, seed, device="cuda"):
 
 
 def attention(q, cache, table, lens, cu, scale=None, window=0, sinks=0):
-    """(out, size, score size, floor): the result in binary64; per element the sum of p_j |vhat_j|,
+    """(out, size, score size, floor, score rms): the result in binary64; per element the sum of p_j |vhat_j|,
     the terms a kernel adds; the largest sum of a score's terms (those of q.c and of z sum(q)); per
     element max s_j sum |c_j - z_j| of the values. Rows outside the sequences are NaN."""
     q, table = q.double().cpu(), table.cpu()
@@ -31,7 +31,7 @@ def attention(q, cache, table, lens, cu, scale=None, window=0, sinks=0):
     scale = 1 / math.sqrt(d) if scale is None else scale
     out = torch.full((tokens, hq, d), math.nan, dtype=torch.float64)
     size, floor = torch.zeros_like(out), torch.zeros_like(out)
-    score_size = 0.0
+    score_size, score_rms = 0.0, 0.0
     for b, n in enumerate(lens):
         n = min(max(n, 0), table.shape[1] * page)
         nq = cu[b + 1] - cu[b]
@@ -67,7 +67,8 @@ def attention(q, cache, table, lens, cu, scale=None, window=0, sinks=0):
                 floor[t, g * group:(g + 1) * group] = vs[at, g].max() * (vu[at, g] - vz[at, g]).abs().sum(0)
                 terms = (rows_q.abs() @ ku[at, g].T + rows_q.sum(1).abs()[:, None] * kz[at, g].T) * ks[at, g].T * scale
                 score_size = max(score_size, float(terms.max()))
-    return out, size, score_size, floor
+                score_rms = max(score_rms, float((rows_q ** 2 @ (k ** 2).T).max()) ** 0.5 * scale)
+    return out, size, score_size, floor, score_rms
 
 
 def check_attention(got, ref, what=""):
@@ -83,11 +84,17 @@ def check_attention(got, ref, what=""):
     rounded sums of 2^-24 per join: 2^-17 covers both with a value sum of up to 64 such steps, and
     2^-14 the long chain. A weight's fp16 terms end at steps of 2^-24: with the row's reference such
     that the largest weight of its block's largest value scale is 2^8 or more, half of that is 2^-33
-    of the largest weight, for each slot: 2^-33 * floor."""
-    out, size, s, floor = ref
+    of the largest weight, for each slot: 2^-33 * floor.
+
+    The kernel for chunks of prompts ("prefill", bf16 results) rounds (c - z) s of the keys to fp16:
+    128 independent errors of at most half a step, 2^-11, so a score is off by a sum of standard
+    deviation 2^-11 / sqrt(3) times the root of its squared terms; eight of those, twice as above."""
+    out, size, s, floor, s2 = ref
     got = got.double().cpu()
-    bf16 = what == "bf16"
+    bf16 = what in ("bf16", "prefill")
     eps = 2 * (11 * 2 ** -23 * s + 2 ** -22) + (2 ** -11 + 2 ** -14 if bf16 else 2 ** -22 + 2 ** -17)
+    if what == "prefill":
+        eps += 2 * 8 * 2 ** -11 / 3 ** 0.5 * s2
     rows = ~torch.isnan(out[:, 0, 0])
     tol = eps * size + 2 ** -33 * floor + (2 ** -8 * out.abs() if bf16 else 0)
     bad = ((got - out).abs() > tol + 1e-30)[rows]

@@ -81,6 +81,68 @@ def test_windows_and_sinks(spin_gpu, window, sinks, nq):
     both(spin_gpu, [333, 50, 1024], [nq, nq, 1], 8, 2, 16, seed=window % 97 + nq, window=window, sinks=sinks)
 
 
+def prefill(spin, lens, nq, hq, hkv, page, seed, **kw):
+    """Calls with enough rows for the kernel for chunks of prompts (74 blocks of 256)."""
+    assert hkv * sum(nq) * (hq // hkv) // 256 >= 74
+    q, cache, table, cu = make(lens, nq, hq, hkv, page, seed)
+    want = ref.attention(q, cache, table, lens, cu, **kw)
+    got = run(spin, q, cache, table, lens, cu, out_dtype=torch.bfloat16, **kw)
+    ref.check_attention(got, want, "prefill")
+    assert spin.device_status() == 0
+    return q, cache, table, cu, got
+
+
+@pytest.mark.parametrize("lens,nq,page", [([700, 333, 5], [300, 333, 1], 64), ([640], [640], 16),
+                                          ([129, 400, 90, 0, 257], [128, 300, 90, 0, 129], 32),
+                                          ([1300, 64], [592, 16], 128)])
+def test_chunks_of_prompts(spin_gpu, lens, nq, page):
+    prefill(spin_gpu, lens, nq, 32, 8, page, seed=page)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (100, 0), (100, 3), (128, 130), (300, 500), (2 ** 31 - 1, 4)])
+def test_chunks_of_prompts_windows(spin_gpu, window, sinks):
+    prefill(spin_gpu, [900, 400], [400, 300], 32, 8, 32, seed=window % 89, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("hq,hkv,n", [(64, 8, 310), (12, 4, 1600), (8, 8, 2400), (40, 1, 500)])
+def test_chunks_of_prompts_head_groupings(spin_gpu, hq, hkv, n):
+    prefill(spin_gpu, [n + 77], [n], hq, hkv, 64, seed=hq)
+
+
+def test_chunks_of_prompts_longer_than_the_cache(spin_gpu):
+    """Tokens before the first slot give 0, in a half, a block and a sequence of their own."""
+    q, cache, table, cu, got = prefill(spin_gpu, [100, 20], [500, 120], 32, 8, 64, seed=3)
+    assert (got[:400] == 0).all() and (got[500:600] == 0).all() and (got[400] != 0).any()
+
+
+def test_chunks_of_prompts_masked_slots_may_hold_anything(spin_gpu):
+    lens, nq = [500, 700], [300, 400]
+    q, cache, table, cu = make(lens, nq, 32, 8, 32, seed=5)
+    kw = dict(window=100, sinks=40)
+    want = ref.attention(q, cache, table, lens, cu, **kw)
+    for name, bad in zip(ref.STEPS, (math.nan, math.inf, -math.inf, math.nan)):
+        cache[name][table[0, 15].item(), :, 20:] = bad  # behind slot 500
+        cache[name][table[0, 1].item(), :, 8:] = bad    # between the sinks and the first window (101)
+        cache[name][table[0, 3].item(), :, :5] = bad    # slots 96 .. 100
+    table[0, 2] = -1
+    table[1, 2:6] = 10 ** 6
+    out = torch.full((700, 32, 128), -7.0, dtype=torch.bfloat16, device="cuda")
+    got = run(spin_gpu, q, cache, table, lens, cu, out=out, **kw)
+    ref.check_attention(got, want, "prefill")
+    # a page gone from the middle of what is seen
+    table[0, 10] = -1
+    ref.check_attention(run(spin_gpu, q, cache, table, lens, cu, out_dtype=torch.bfloat16, **kw),
+                        ref.attention(q, cache, table, lens, cu, **kw), "prefill")
+
+
+def test_chunks_of_prompts_beside_single_tokens(spin_gpu):
+    """One call with chunks, drafted tokens and single tokens: both kernels, twice the same bits."""
+    lens, nq = [800, 333, 64, 2000, 17, 1500], [400, 1, 64, 3, 17, 200]
+    q, cache, table, cu, got = prefill(spin_gpu, lens, nq, 32, 8, 64, seed=6)
+    again = run(spin_gpu, q, cache, table, lens, cu, out_dtype=torch.bfloat16)
+    assert torch.equal(got, again)
+
+
 def test_long_sequences_are_cut_and_joined(spin_gpu):
     """Enough units that items are cut over many thread blocks, and several pieces per item."""
     both(spin_gpu, [40000, 9, 12345], [1, 1, 1], 8, 2, 128, seed=11)
