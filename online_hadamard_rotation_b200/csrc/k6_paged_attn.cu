@@ -52,7 +52,7 @@
 // 2^-33 of the row's largest weight or less.
 //
 // Work is divided over a fixed number of warps: the list of all (sequence, kv head, row tile)
-// items, each as many units long as its sequence has slot blocks and kItem more for its fixed
+// items, each as many units long as its sequence has slot blocks and cuts.item more for its fixed
 // cost, is cut into equal runs, one per warp; cuts near an item's end move to that end. A warp
 // writes an item that lies inside its run at once and leaves the pieces of cut ones in shared
 // memory, where the block joins what its warps share; pieces of items that reach other blocks
@@ -79,9 +79,8 @@ constexpr int kD = 128;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCtas = 600;  // most blocks of a launch (sets the workspace)
-constexpr int kItem = 2;       // units an item costs besides its slot blocks
-constexpr int kSnap = 3;  // cuts this close to an item's end move there
-constexpr int kMinRun = 4;     // shortest run worth a warp of its own
+constexpr Cuts kCoarse = {2, 3, 4};  // where every warp has several blocks
+constexpr Cuts kFine = {0, 1, 1};    // where there are fewer blocks than warps: one each, latency counts
 constexpr int kNarrowRows = 64;  // rows of a sequence (tokens x group) that are this kernel's in any call
 constexpr int kPart = 132;     // floats per row of a piece: 128 sums, max, sum of weights, pad
 constexpr float kRoom = 9.0f;   // a raised reference leaves weights at most 2^kRoom
@@ -100,6 +99,10 @@ __device__ __forceinline__ Blocks seq_blocks(const PagedArgs &a, const Seq &s) {
   r.nsink = a.window > 0 ? min((min(a.sinks, s.len) + BS - 1) / BS, r.first) : 0;
   r.count = r.nsink + end - r.first;
   return r;
+}
+
+__device__ __forceinline__ int item_units(const PagedArgs &a, const Blocks &bl) {
+  return max(1, bl.count + a.cuts.item);  // an item of no blocks writes its zeros
 }
 
 template <int R>
@@ -231,6 +234,7 @@ struct alignas(16) Smem {
   long long before[kThreads], cut[kWarps + 1], base[kWarps];
   int seq[kWarps];
   Piece piece[kWarps][2];
+  alignas(16) float head[kWarps][R][kPart];
 };
 
 // x / y and x % y; 32-bit where the counts allow it.
@@ -249,10 +253,9 @@ struct Worker {
   int warp, lane, g, c;
 
   // Row `row` of piece k (0: of an item begun by an earlier warp, 1: of one begun by this warp) of
-  // a warp: in the workspace, or in the place of the warp's stage.
+  // a warp, the latter in the place of the warp's stage.
   __device__ __forceinline__ float *piece_row(int of_warp, int k, int row) const {
-    return k == 0 ? a.heads + (((int64_t)blockIdx.x * kWarps + of_warp) * R + row) * kPart
-                  : sm.block[of_warp].tail[row];
+    return k == 0 ? sm.head[of_warp][row] : sm.block[of_warp].tail[row];
   }
 
   // Row tile `rt` of kv head `h` and sequence `s`: rows' queries as B fragments, their sums,
@@ -355,7 +358,7 @@ struct Worker {
     auto start_of = [&](int k) { return (k < bl.nsink ? k : k - bl.nsink + bl.first) * BS; };
     // this tile's part of the sequence's blocks: not behind its last row, nor before its first
     // row's window
-    int i = max(off - kItem, 0), end = off + cnt - kItem;
+    int i = max(off - a.cuts.item, 0), end = off + cnt - a.cuts.item;
     while (end > i && start_of(end - 1) > last_pos) --end;
     while (i < end && start_of(i) >= a.sinks && a.window > 0 && start_of(i) + BS - 1 <= first_pos - a.window) ++i;
 
@@ -612,7 +615,7 @@ struct Worker {
     }
 
     // ---- row sums over the groups; then the result, or a piece of it
-    const bool begins = off == 0, ends = off + cnt == bl.count + kItem;
+    const bool begins = off == 0, ends = off + cnt == item_units(a, bl);
     const int slot = begins ? 1 : 0;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -670,13 +673,16 @@ struct Worker {
     for (int i = threadIdx.x; i < p.rows * (kD / 4); i += kThreads) {
       const int row = i / (kD / 4), e = 4 * (i % (kD / 4));
       float top = -INFINITY;
-      for (int k = first; k <= last; ++k)
-        if (sm.piece[k >> 1][k & 1].rows > 0) top = fmaxf(top, piece_row(k >> 1, k & 1, row)[kD]);
+#pragma unroll
+      for (int k = 0; k < 2 * kWarps; ++k)
+        if (k >= first && k <= last && sm.piece[k >> 1][k & 1].rows > 0)
+          top = fmaxf(top, piece_row(k >> 1, k & 1, row)[kD]);
       float den = 0.0f;
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int k = first; k <= last; ++k) {
+#pragma unroll
+      for (int k = 0; k < 2 * kWarps; ++k) {
         const float *part = piece_row(k >> 1, k & 1, row);
-        if (sm.piece[k >> 1][k & 1].rows == 0 || part[kD] == -INFINITY) continue;
+        if (k < first || k > last || sm.piece[k >> 1][k & 1].rows == 0 || part[kD] == -INFINITY) continue;
         const float f = ex2(part[kD] - top);
         const float4 x = *reinterpret_cast<const float4 *>(part + e);
         den = fmaf(part[kD + 1], f, den);
@@ -718,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k6_paged_attn(const
   const int per = (a.seqs + kThreads - 1) / kThreads;
   const int b0 = min(t * per, a.seqs), b1 = min(b0 + per, a.seqs);
   auto units = [&](const Seq &s, const Blocks &bl) {
-    return (long long)a.hkv * row_tiles<R>(a, s) * (bl.count + kItem);
+    return (long long)a.hkv * row_tiles<R>(a, s) * item_units(a, bl);
   };
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
@@ -741,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k6_paged_attn(const
     total += sm.scan[w];
   }
   const long long workers = (long long)gridDim.x * kWarps;
-  const long long run = max(quot(total + workers - 1, workers), (long long)kMinRun);
+  const long long run = max(quot(total + workers - 1, workers), (long long)a.cuts.min_run);
   // ---- the cuts between this block's warps, moved to an item's end where one is near: thread e
   // finds cut e, first the thread whose sequences hold it, then the sequence
   sm.before[t] = before;
@@ -762,8 +768,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k6_paged_attn(const
         const Blocks bl = seq_blocks<BS>(a, s);
         const long long n = units(s, bl);
         if (u < base + n) {
-          const int len = bl.count + kItem, in = rem(u - base, len);
-          cut = in < kSnap ? u - in : len - in < kSnap ? u - in + len : u;
+          const int len = item_units(a, bl), in = rem(u - base, len);
+          cut = in < a.cuts.snap ? u - in : len - in < a.cuts.snap ? u - in + len : u;
           if (t < kWarps) {
             sm.seq[t] = b;
             sm.base[t] = base;
@@ -791,14 +797,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k6_paged_attn(const
         ++b;
         continue;
       }
-      const int tiles = row_tiles<R>(a, s), len = bl.count + kItem;
+      const int tiles = row_tiles<R>(a, s), len = item_units(a, bl);
       const long long item = quot(u - base, len);
       const int off = (int)((u - base) - item * len);
       const int h = (int)quot(item, tiles), rt = (int)(item - (long long)h * tiles);
       const int cnt = (int)min((long long)(len - off), u1 - u);
       int blocks = 1;
       if (off == 0 && cnt < len) {  // the cuts inside the item, by the rule above, end at warp `last`
-        const long long last = quot(u + len - kSnap, run);
+        const long long last = quot(u + len - a.cuts.snap, run);
         blocks = (int)(last / kWarps - blockIdx.x + 1);
       }
       w.run(s, bl, b, h, rt, off, cnt, blocks);
@@ -890,16 +896,17 @@ cudaError_t launch(PagedArgs a, void *workspace, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // units there can be at most, so that small calls launch few blocks
   const int64_t tiles = (int64_t)a.seqs + (int64_t)a.tokens * a.group / R;
-  const int64_t blocks = ((int64_t)a.cap + BS - 1) / BS + 1 + kItem;
-  const int64_t most = ((int64_t)a.hkv * tiles * blocks + kMinRun * kWarps - 1) / (kMinRun * kWarps);
+  const int64_t blocks = ((int64_t)a.cap + BS - 1) / BS + 1;
   int64_t grid = slots < kMaxCtas ? slots : kMaxCtas;
+  a.cuts = (int64_t)a.hkv * tiles * blocks <= grid * kWarps ? kFine : kCoarse;
+  const int64_t least = a.cuts.min_run * kWarps;  // units worth a block
+  const int64_t most = ((int64_t)a.hkv * tiles * (blocks + a.cuts.item) + least - 1) / least;
   if (most < grid) grid = most;
   a.parts = static_cast<float *>(workspace);
-  a.heads = a.parts + (int64_t)kMaxCtas * 2 * R * kPart;
-  a.recs = reinterpret_cast<int4 *>(a.heads + (int64_t)kMaxCtas * kWarps * R * kPart);
+  a.recs = reinterpret_cast<int4 *>(a.parts + (int64_t)kMaxCtas * 2 * R * kPart);
   k6_paged_attn<NT, MT, F32><<<(unsigned)grid, kThreads, smem, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (blocks < 2 * kSnap || grid == 1) return cudaSuccess;  // no item can reach two blocks
+  if (blocks + a.cuts.item < 2 * a.cuts.snap || grid == 1) return cudaSuccess;  // no item can reach two blocks
   // the join's blocks are placed while the first kernel drains and wait for its end
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
@@ -922,7 +929,7 @@ int rows_per_tile(int group, int max_q_len) {
 
 size_t paged_attention_workspace_bytes(int group, int max_q_len) {
   const size_t r = (size_t)rows_per_tile(group, max_q_len);
-  return (size_t)kMaxCtas * ((2 + kWarps) * r * kPart * sizeof(float) + sizeof(int4));
+  return (size_t)kMaxCtas * (2 * r * kPart * sizeof(float) + sizeof(int4));
 }
 
 cudaError_t launch_paged_attention(const PagedAttention &p, cudaStream_t stream) {
@@ -951,7 +958,6 @@ cudaError_t launch_paged_attention(const PagedAttention &p, cudaStream_t stream)
   a.sinks = p.sinks < a.cap ? p.sinks : a.cap;
   a.scale_log2 = p.softmax_scale * 1.4426950408889634f;
   a.out = p.out;
-  const bool one = rows_per_tile(a.group, p.max_q_len) == 8;
   a.row_limit = INT_MAX;
   // chunks of prompts go to the tensor-memory kernel, other sequences of the same call (if there
   // can be any) stay here; fp32 results do too, whose weights want two terms
@@ -961,6 +967,9 @@ cudaError_t launch_paged_attention(const PagedAttention &p, cudaStream_t stream)
     const cudaError_t e = launch_paged_prefill(a, stream);
     if (e != cudaSuccess) return e;
   }
+  // (32 rows a tile would expand the codes once for all of them, but at 255 registers and eight
+  // warps an SM: 88 us against 71 for four drafted tokens of 16 sequences, 8 heads per kv head)
+  const bool one = rows_per_tile(a.group, p.max_q_len) == 8;
   if (p.out_f32)
     return one ? launch<1, 4, true>(a, p.workspace, stream) : launch<2, 2, true>(a, p.workspace, stream);
   return one ? launch<1, 4, false>(a, p.workspace, stream) : launch<2, 2, false>(a, p.workspace, stream);

@@ -10,6 +10,12 @@
 
 namespace spin {
 
+// How the narrow kernel cuts its work into runs: units an item costs besides its slot blocks, how
+// close to an item's end a cut moves to it, the shortest run worth a warp of its own.
+struct Cuts {
+  int item, snap, min_run;
+};
+
 struct PagedArgs {
   const __nv_bfloat16 *q;
   const uint8_t *kc, *vc;
@@ -17,11 +23,11 @@ struct PagedArgs {
   const int32_t *table, *lens, *cu;
   int tokens, seqs, cols, num_pages, page_shift, cap;  // cap: slots a table row can name
   int hq, hkv, group, window, sinks;
+  Cuts cuts;
   int row_limit;  // rows (tokens x group) up to which a sequence is the narrow kernel's
   float scale_log2;  // softmax scale x log2(e)
   void *out;
   float *parts;  // [grid][2][R][kPart]
-  float *heads;  // [grid][kWarps][R][kPart], read by the block that wrote them
   int4 *recs;    // [grid]
 };
 
