@@ -429,8 +429,8 @@ typedef struct spin_kv_pages_t {
  *  window       >= 0, 0 for none; sinks >= 0 (without a window they change nothing)
  *  out          [tokens, n_q_heads, head_dim] bf16 or fp32 (out_dtype), 16-byte aligned
  *  workspace    caller-owned device scratch of at least
- *               spin_paged_attention_workspace_bytes(n_q_heads, n_kv_heads, max_q_len) bytes,
- *               16-byte aligned, contents on entry do not matter; calls (and captured graphs)
+ *               spin_paged_attention_workspace_bytes(n_q_heads, n_kv_heads, max_q_len,
+ *               table_cols * page_size) bytes (may be NULL where that is 0), 16-byte aligned, contents on entry do not matter; calls (and captured graphs)
  *               that may run at the same time need separate workspaces
  * block_table, lens and cu_q are read on the device: a captured graph may be replayed after
  * their contents (not their sizes) change. seqs == 0 or tokens == 0 is a no-op.
@@ -445,9 +445,11 @@ spin_status_t spin_paged_attention_int4kv(const void *q, int32_t tokens, const s
                                           void *out, int32_t out_dtype, void *workspace, size_t workspace_bytes,
                                           spin_stream_t stream);
 
-/* Workspace bytes spin_paged_attention_int4kv needs: two pieces of a row tile per thread
- * block, whatever the lengths; 0 for sizes <= 0 or n_q_heads % n_kv_heads != 0. */
-size_t spin_paged_attention_workspace_bytes(int32_t n_q_heads, int32_t n_kv_heads, int32_t max_q_len);
+/* Workspace bytes spin_paged_attention_int4kv needs: two pieces of a row tile per thread block,
+ * whatever the lengths, or 0 where rows are too short for pieces (cache_slots, table_cols *
+ * page_size, below about 400) and for sizes <= 0 or n_q_heads % n_kv_heads != 0. */
+size_t spin_paged_attention_workspace_bytes(int32_t n_q_heads, int32_t n_kv_heads, int32_t max_q_len,
+                                            int64_t cache_slots);
 
 /*
  * Copy whole pages: page dst_pages[i] of `dst` <- page src_pages[i] of `src`, codes, scales and

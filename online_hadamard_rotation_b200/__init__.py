@@ -85,7 +85,7 @@ def lib() -> C.CDLL:
     kv = pool = C.c_char_p  # packed spin_kv_pages_t and spin_kv_pool_t
     L.spin_paged_attention_int4kv.argtypes = [vp, i32, kv, vp, i32, i32, vp, vp, i32, i32, f32, i32, i32, vp, i32, vp,
                                               C.c_size_t, vp]
-    L.spin_paged_attention_workspace_bytes.argtypes = [i32, i32, i32]
+    L.spin_paged_attention_workspace_bytes.argtypes = [i32, i32, i32, i64]
     L.spin_paged_attention_workspace_bytes.restype = C.c_size_t
     L.spin_kv_pages_copy.argtypes = [kv, vp, kv, vp, i32, vp]
     L.spin_kv_slots_copy.argtypes = [kv, vp, i32, vp, vp, i32, i32, kv, vp, i32, vp, vp]
@@ -543,9 +543,16 @@ def _pages(cache: dict, what: str = "cache"):
     return _pack_pages(*ptrs, shape[0], shape[1], shape[2], 2 * shape[3]), device, shape
 
 
-def _pool(pool: dict, block_table: torch.Tensor, lens: torch.Tensor):
-    """(packed cache, packed pool, device index, table pointer, rows, cols, lens pointer)"""
-    kv, device, shape = _pages(pool, "pool")
+def _pool(pool: dict, block_table: torch.Tensor, lens: torch.Tensor, moves: bool = False):
+    """(packed cache, packed pool, device index, table pointer, rows, cols, lens pointer). Only a
+    call that moves slots takes the cache's pointers; the others need its sizes."""
+    if moves:
+        kv, device, shape = _pages(pool, "pool")
+    else:
+        shape, device = pool["k_cache"].shape, pool["k_cache"].get_device()
+        if len(shape) != 4 or device < 0:
+            raise ValueError("pool: k_cache must be a [pages, n_kv_heads, page_size, head_dim / 2] CUDA tensor")
+        kv = _pack_pages(0, 0, 0, 0, 0, 0, shape[0], shape[1], shape[2], 2 * shape[3])
     packed = _pack_pool(_vec(pool["refs"], "refs", device, shape[0]),
                         _vec(pool["free_pages"], "free_pages", device, shape[0]),
                         _vec(pool["free_count"], "free_count", device, 1))
@@ -564,9 +571,12 @@ def alloc_kv_pages(pages: int, n_kv_heads: int, page_size: int = 64, head_dim: i
     return pool
 
 
-def paged_attention_workspace_bytes(n_q_heads: int, n_kv_heads: int, max_q_len: int = 1) -> int:
-    """Scratch bytes paged_attention_int4kv needs (see spin_paged_attention_workspace_bytes)."""
-    return int(lib().spin_paged_attention_workspace_bytes(int(n_q_heads), int(n_kv_heads), int(max_q_len)))
+def paged_attention_workspace_bytes(n_q_heads: int, n_kv_heads: int, max_q_len: int = 1,
+                                    cache_slots: int = 2 ** 31 - 1) -> int:
+    """Scratch bytes paged_attention_int4kv needs for tables of cache_slots slots a row (cols *
+    page_size; see spin_paged_attention_workspace_bytes)."""
+    return int(lib().spin_paged_attention_workspace_bytes(int(n_q_heads), int(n_kv_heads), int(max_q_len),
+                                                          int(cache_slots)))
 
 
 def paged_attention_int4kv(q: torch.Tensor, cache: dict, block_table: torch.Tensor, lens: torch.Tensor,
@@ -600,14 +610,18 @@ def paged_attention_int4kv(q: torch.Tensor, cache: dict, block_table: torch.Tens
         out = _empty((tokens, hq, d), out_dtype, device, stream)
     else:
         _rows(out, "out", out_dtype, device, (tokens, hq, d))
-    if workspace is None:
-        need = lib().spin_paged_attention_workspace_bytes(hq, shape[1], max_q_len)
-        workspace = _empty((max(need, 16),), _U8, device, stream)
-    else:
+    ws_at = ws_bytes = 0
+    if workspace is not None:
         _rows(workspace, "workspace", _U8, device, workspace.shape)
+    else:
+        ws_bytes = lib().spin_paged_attention_workspace_bytes(hq, shape[1], max_q_len, cols * shape[2])
+        if ws_bytes:  # short rows need none
+            workspace = _empty((ws_bytes,), _U8, device, stream)
+    if workspace is not None:
+        ws_at, ws_bytes = workspace.data_ptr(), workspace.numel()
     _call("spin_paged_attention_int4kv", device, stream, q.data_ptr(), tokens, kv, table, seqs, cols, lens_at, cu_at,
           max_q_len, hq, d ** -0.5 if softmax_scale is None else softmax_scale, window, sinks, out.data_ptr(),
-          F32 if out_dtype is torch.float32 else BF16, workspace.data_ptr(), workspace.numel())
+          F32 if out_dtype is torch.float32 else BF16, ws_at, ws_bytes)
     return out
 
 
@@ -684,7 +698,7 @@ def fork_kv_pages(pool: dict, block_table: torch.Tensor, lens: torch.Tensor, par
     filled slots of a partly filled last page are copied into a page of the child's own. Returns
     int32 [n]: KV_OK, KV_NO_PAGES, or KV_REFUSED (bad index, a child that is not empty or was
     claimed by an earlier fork of the call)."""
-    kv, p, device, table, rows, cols, lens_at = _pool(pool, block_table, lens)
+    kv, p, device, table, rows, cols, lens_at = _pool(pool, block_table, lens, moves=True)
     n = parents.numel()
     parents_at = _vec(parents, "parents", device, n)
     children_at = _vec(children, "children", device, n)

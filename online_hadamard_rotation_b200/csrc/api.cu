@@ -289,9 +289,10 @@ spin_status_t spin_dequant_hadamard_inverse(const uint8_t *codes, int64_t rows, 
                                             out_dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-size_t spin_paged_attention_workspace_bytes(int32_t n_q_heads, int32_t n_kv_heads, int32_t max_q_len) {
-  if (n_q_heads <= 0 || n_kv_heads <= 0 || max_q_len <= 0 || n_q_heads % n_kv_heads != 0) return 0;
-  return paged_attention_workspace_bytes(n_q_heads / n_kv_heads, max_q_len);
+size_t spin_paged_attention_workspace_bytes(int32_t n_q_heads, int32_t n_kv_heads, int32_t max_q_len,
+                                            int64_t cache_slots) {
+  if (n_q_heads <= 0 || n_kv_heads <= 0 || max_q_len <= 0 || cache_slots <= 0 || n_q_heads % n_kv_heads != 0) return 0;
+  return paged_attention_workspace_bytes(n_q_heads / n_kv_heads, max_q_len, cache_slots);
 }
 
 spin_status_t spin_paged_attention_int4kv(const void *q, int32_t tokens, const spin_kv_pages_t *cache,
@@ -312,8 +313,9 @@ spin_status_t spin_paged_attention_int4kv(const void *q, int32_t tokens, const s
       (int64_t)cache->pages * cache->n_kv_heads * page >= (int64_t(1) << 31))
     return SPIN_ERR_UNSUPPORTED_SIZE;
   if (seqs == 0 || tokens == 0) return SPIN_OK;
-  if (!q || !block_table || !lens || !out || !workspace ||
-      workspace_bytes < spin_paged_attention_workspace_bytes(n_q_heads, cache->n_kv_heads, max_q_len))
+  const size_t need = spin_paged_attention_workspace_bytes(n_q_heads, cache->n_kv_heads, max_q_len,
+                                                           (int64_t)table_cols * page);
+  if (cache->pages < 1 || !q || !block_table || !lens || !out || workspace_bytes < need || (need > 0 && !workspace))
     return SPIN_ERR_INVALID_ARG;
   if ((st = check_pages_memory(cache)) != SPIN_OK) return st;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || !aligned(block_table, 4) ||

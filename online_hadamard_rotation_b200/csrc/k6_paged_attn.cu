@@ -79,8 +79,9 @@ constexpr int kD = 128;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCtas = 600;  // most blocks of a launch (sets the workspace)
-constexpr Cuts kCoarse = {2, 3, 4};  // where every warp has several blocks
-constexpr Cuts kFine = {0, 1, 1};    // where there are fewer blocks than warps: one each, latency counts
+constexpr Cuts kCoarse = {2, 3, 4, 0};  // where every warp has several blocks
+constexpr Cuts kFine = {0, 1, 1, 0};    // where there are fewer blocks than warps: one each, latency counts
+constexpr int kWholeUnits = 16;  // items up to this length stay in one block of threads
 constexpr int kNarrowRows = 64;  // rows of a sequence (tokens x group) that are this kernel's in any call
 constexpr int kPart = 132;     // floats per row of a piece: 128 sums, max, sum of weights, pad
 constexpr float kRoom = 9.0f;   // a raised reference leaves weights at most 2^kRoom
@@ -748,12 +749,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k6_paged_attn(const
   }
   const long long workers = (long long)gridDim.x * kWarps;
   const long long run = max(quot(total + workers - 1, workers), (long long)a.cuts.min_run);
-  // ---- the cuts between this block's warps, moved to an item's end where one is near: thread e
-  // finds cut e, first the thread whose sequences hold it, then the sequence
+  // ---- the cuts between this block's warps: thread e finds cut e, first the thread whose sequences
+  // hold it, then the sequence
   sm.before[t] = before;
   __syncthreads();
-  if (t <= kWarps) {
-    const long long u = ((long long)blockIdx.x * kWarps + t) * run;
+  auto find = [&](int e, long long u, bool to_item) {
     long long cut = total;
     if (u < total) {
       int lo = 0, hi = kThreads - 1;  // the last thread with before <= u (later ones of the same value are empty)
@@ -769,17 +769,29 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k6_paged_attn(const
         const long long n = units(s, bl);
         if (u < base + n) {
           const int len = item_units(a, bl), in = rem(u - base, len);
-          cut = in < a.cuts.snap ? u - in : len - in < a.cuts.snap ? u - in + len : u;
-          if (t < kWarps) {
-            sm.seq[t] = b;
-            sm.base[t] = base;
+          const bool back = to_item ? 2 * in < len : in < a.cuts.snap;
+          const bool on = to_item ? !back : len - in < a.cuts.snap;
+          cut = back ? u - in : on ? u - in + len : u;
+          if (e < kWarps) {
+            sm.seq[e] = b;
+            sm.base[e] = base;
           }
           break;
         }
         base += n;
       }
     }
-    sm.cut[t] = cut;
+    sm.cut[e] = cut;
+  };
+  const long long u0 = (long long)blockIdx.x * kWarps * run;
+  if (a.cuts.whole) {
+    // short items stay in one block: its ends move to the nearest item's, its warps share what is between
+    if (t < 2) find(t * kWarps, u0 + t * kWarps * run, true);
+    __syncthreads();
+    const long long c0 = sm.cut[0], c1 = sm.cut[kWarps];
+    if (t > 0 && t < kWarps) find(t, c0 + quot((c1 - c0) * t, kWarps), false);
+  } else {
+    if (t <= kWarps) find(t, u0 + t * run, false);
   }
   __syncthreads();
   Worker<NT, MT, F32> w{a, sm, warp, lane, lane >> 2, lane & 3};
@@ -803,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k6_paged_attn(const
       const int h = (int)quot(item, tiles), rt = (int)(item - (long long)h * tiles);
       const int cnt = (int)min((long long)(len - off), u1 - u);
       int blocks = 1;
-      if (off == 0 && cnt < len) {  // the cuts inside the item, by the rule above, end at warp `last`
+      if (off == 0 && cnt < len && !a.cuts.whole) {  // the cuts inside the item, by the rule above, end at warp `last`
         const long long last = quot(u + len - a.cuts.snap, run);
         blocks = (int)(last / kWarps - blockIdx.x + 1);
       }
@@ -829,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k6_paged_attn(const
     if (p.begins && !ends) rec = make_int4(p.blocks, p.seq, p.head, p.tile);
     k = last + 1;
   }
-  if (t == 0) a.recs[blockIdx.x] = rec;
+  if (t == 0 && !a.cuts.whole) a.recs[blockIdx.x] = rec;  // a call of short items has no workspace
 }
 
 // Joins the pieces of the item that was cut where block x's run ended: out = sum_c
@@ -886,6 +898,9 @@ __global__ void __launch_bounds__(R * kD / 4) k6_paged_join(const PagedArgs a) {
         make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
+// Items of at most this many blocks are not cut between thread blocks.
+bool whole_items(int64_t blocks, const Cuts &cuts) { return blocks + cuts.item <= kWholeUnits; }
+
 template <int NT, int MT, bool F32>
 cudaError_t launch(PagedArgs a, void *workspace, cudaStream_t stream) {
   constexpr int R = 8 * NT, BS = 16 * MT;
@@ -899,6 +914,7 @@ cudaError_t launch(PagedArgs a, void *workspace, cudaStream_t stream) {
   const int64_t blocks = ((int64_t)a.cap + BS - 1) / BS + 1;
   int64_t grid = slots < kMaxCtas ? slots : kMaxCtas;
   a.cuts = (int64_t)a.hkv * tiles * blocks <= grid * kWarps ? kFine : kCoarse;
+  a.cuts.whole = whole_items(blocks, a.cuts);
   const int64_t least = a.cuts.min_run * kWarps;  // units worth a block
   const int64_t most = ((int64_t)a.hkv * tiles * (blocks + a.cuts.item) + least - 1) / least;
   if (most < grid) grid = most;
@@ -906,7 +922,7 @@ cudaError_t launch(PagedArgs a, void *workspace, cudaStream_t stream) {
   a.recs = reinterpret_cast<int4 *>(a.parts + (int64_t)kMaxCtas * 2 * R * kPart);
   k6_paged_attn<NT, MT, F32><<<(unsigned)grid, kThreads, smem, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (blocks + a.cuts.item < 2 * a.cuts.snap || grid == 1) return cudaSuccess;  // no item can reach two blocks
+  if (a.cuts.whole || grid == 1) return cudaSuccess;  // no item reaches two blocks
   // the join's blocks are placed while the first kernel drains and wait for its end
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
@@ -927,9 +943,11 @@ int rows_per_tile(int group, int max_q_len) {
 
 }  // namespace
 
-size_t paged_attention_workspace_bytes(int group, int max_q_len) {
-  const size_t r = (size_t)rows_per_tile(group, max_q_len);
-  return (size_t)kMaxCtas * (2 * r * kPart * sizeof(float) + sizeof(int4));
+size_t paged_attention_workspace_bytes(int group, int max_q_len, int64_t cache_slots) {
+  const int r = rows_per_tile(group, max_q_len);
+  // whole_items with the larger of the two cuts' costs and the smallest block of slots
+  if (whole_items((cache_slots + 31) / 32 + 1, kCoarse)) return 0;
+  return (size_t)kMaxCtas * (2 * (size_t)r * kPart * sizeof(float) + sizeof(int4));
 }
 
 cudaError_t launch_paged_attention(const PagedAttention &p, cudaStream_t stream) {

@@ -83,7 +83,7 @@ struct PagedAttention {
   bool out_f32;
   void *workspace;
 };
-size_t paged_attention_workspace_bytes(int group, int max_q_len);
+size_t paged_attention_workspace_bytes(int group, int max_q_len, int64_t cache_slots);
 cudaError_t launch_paged_attention(const PagedAttention &p, cudaStream_t stream);
 cudaError_t read_prefill_status(unsigned int *status, bool reset);  // k8_paged_prefill.cu
 // W4A4 GEMM on packed INT4 codes (k5_w4a4_gemm.cu): shapes it takes (n_out a multiple

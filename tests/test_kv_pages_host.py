@@ -32,7 +32,7 @@ def pool(**kw):
 
 
 def attn(L, cache=None, **kw):
-    a = dict(q=FAKE, tokens=4, table=FAKE, seqs=2, cols=8, lens=FAKE, cu=FAKE, most=2, hq=32, scale=0.088, window=0,
+    a = dict(q=FAKE, tokens=4, table=FAKE, seqs=2, cols=800, lens=FAKE, cu=FAKE, most=2, hq=32, scale=0.088, window=0,
              sinks=0, out=FAKE, dtype=1, ws=FAKE, bytes=1 << 30)
     a.update(kw)
     return L.spin_paged_attention_int4kv(a["q"], a["tokens"], cache or pages(), a["table"], a["seqs"], a["cols"],
@@ -64,9 +64,11 @@ def test_attention_rules(L):
 
 def test_workspace_bytes(L):
     f = L.spin_paged_attention_workspace_bytes
-    assert f(32, 8, 1) > 0 and f(32, 8, 1) % 16 == 0
-    assert f(32, 8, 1) <= f(32, 8, 4) <= f(32, 8, 100) == f(32, 8, 1 << 30)
-    assert f(0, 8, 1) == f(32, 0, 1) == f(32, 8, 0) == f(30, 8, 1) == f(-32, -8, 1) == 0
+    n = 1 << 40
+    assert f(32, 8, 1, n) > 0 and f(32, 8, 1, n) % 16 == 0 and f(32, 8, 1, 4096) == f(32, 8, 1, n)
+    assert f(32, 8, 1, n) <= f(32, 8, 4, n) <= f(32, 8, 100, n) == f(32, 8, 1 << 30, n)
+    assert f(0, 8, 1, n) == f(32, 0, 1, n) == f(32, 8, 0, n) == f(30, 8, 1, n) == f(-32, -8, 1, n) == f(32, 8, 1, 0) == 0
+    assert f(32, 8, 1, 64) == 0  # a short row is never cut
 
 
 def test_copy_rules(L):
