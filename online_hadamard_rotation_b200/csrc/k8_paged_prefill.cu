@@ -107,6 +107,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
@@ -135,6 +140,32 @@ __device__ __forceinline__ uint4 codes8(uint32_t w, uint32_t zero) {
 // rows of 128 bytes, 128-byte swizzle.
 __device__ __forceinline__ uint32_t piece_at(uint32_t r, uint32_t j) {
   return (j >> 3) * (kTile * 128u) + r * 128u + (((j & 7u) ^ (r & 7u)) << 4);
+}
+
+// Loads that stay where they are written: two tiles before their use.
+__device__ __forceinline__ uint4 load16_ahead(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ __half load_half_ahead(const __half *p) {
+  unsigned short v;
+  asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return __ushort_as_half(v);
+}
+__device__ __forceinline__ int load_ahead(const int32_t *p) {
+  int v;
+  asm volatile("ld.global.nc.L1::no_allocate.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
+// Scores of hidden slots (bits of v0, v1 that are not set) become -inf.
+__device__ __forceinline__ void hide(uint32_t (&x)[64], uint32_t v0, uint32_t v1) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    x[k] = (v0 >> k & 1u) ? x[k] : 0xFF800000u;
+    x[32 + k] = (v1 >> k & 1u) ? x[32 + k] : 0xFF800000u;
+  }
 }
 
 struct Slot {  // what a converter holds of its slot of a tile
@@ -274,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
       const int j0 = start_of(i);
       const float f = qmul * S.kscale[st];
       const float vexp = S.vexp[st];
-      const uint32_t seen[4] = {S.seen[st][0], S.seen[st][1], S.seen[st][2], S.seen[st][3]};
+      const uint32_t *seen = S.seen[st];
       const bool all_seen = (seen[0] & seen[1] & seen[2] & seen[3]) == 0xFFFFFFFFu && j0 + kTile - 1 <= lo_pos &&
                             (a.window == 0 || j0 > hi_pos - a.window || j0 + kTile <= a.sinks);
       // slots of 32-slot part c that this row sees, as bits
@@ -288,22 +319,24 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
         if (a.window > 0) v &= ~below(pos - a.window + 1) | below(a.sinks);
         return v & seen[c];
       };
-      // ---- the row's largest score
+      // ---- the row's largest score (its scores are read twice: 128 registers for them would spill,
+      // and what spills is read back through an L1 that shared memory leaves small)
       float top = -INFINITY;
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t x[32];
-        tc::tmem_ld32(s_at + 32u * c, x);
+      for (int c = 0; c < 2; ++c) {
+        uint32_t x[64];
+        tc::tmem_ld32(s_at + 64u * c, x);
+        tc::tmem_ld32(s_at + 64u * c + 32u, x + 32);
         tc::tmem_wait_ld();
-        if (all_seen) {
+        if (!all_seen) hide(x, visible(2 * c), visible(2 * c + 1));
+        float t0 = __uint_as_float(x[0]), t1 = __uint_as_float(x[1]);
 #pragma unroll
-          for (int k = 0; k < 32; k += 2)
-            top = fmaxf(top, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
-        } else {
-          const uint32_t v = visible(c);
-#pragma unroll
-          for (int k = 0; k < 32; ++k) top = fmaxf(top, (v >> k & 1u) ? __uint_as_float(x[k]) : -INFINITY);
+        for (int k = 2; k < 62; k += 4) {
+          t0 = max3(t0, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+          t1 = max3(t1, __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
         }
+        t0 = max3(t0, __uint_as_float(x[62]), __uint_as_float(x[63]));
+        top = max3(top, t0, t1);
       }
       top = fmaf(top, f, vexp);
       // ---- raise the reference where a weight could exceed it by too much
@@ -319,44 +352,42 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
           tc::tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < 8; ++c) {
-            uint32_t x[16];
-            tmem_ld16(o_at + 16u * c, x);
+            uint32_t o[16];
+            tmem_ld16(o_at + 16u * c, o);
             tc::tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * fac);
-            tmem_st16(o_at + 16u * c, x);
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fac);
+            tmem_st16(o_at + 16u * c, o);
           }
           tmem_wait_st();
         }
       }
-      // ---- weights over the scores: 32 scores become 16 columns that lie before them
+      // ---- weights over the scores: 64 scores become 32 columns that do not reach past them
       const float mr = m == -INFINITY ? 0.0f : m;
-      float l0 = 0.0f, l1 = 0.0f;
+      float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t x[32], p[16];
-        tc::tmem_ld32(s_at + 32u * c, x);
-        const float4 *vs = reinterpret_cast<const float4 *>(&S.vs[st][32 * c]);
+      for (int c = 0; c < 2; ++c) {
+        uint32_t x[64], p[32];
+        tc::tmem_ld32(s_at + 64u * c, x);
+        tc::tmem_ld32(s_at + 64u * c + 32u, x + 32);
+        const float4 *vs = reinterpret_cast<const float4 *>(&S.vs[st][64 * c]);
         tc::tmem_wait_ld();
-        if (!all_seen) {
-          const uint32_t v = visible(c);
+        if (!all_seen) hide(x, visible(2 * c), visible(2 * c + 1));
 #pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = (v >> k & 1u) ? x[k] : 0xFF800000u;
-        }
-#pragma unroll
-        for (int k = 0; k < 32; k += 4) {
+        for (int k = 0; k < 64; k += 4) {
           const float4 s4 = vs[k >> 2];
           const float2 y0 = fma2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), f, -mr);
           const float2 y1 = fma2(make_float2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])), f, -mr);
-          const float p0 = ex2(y0.x), p1 = ex2(y0.y), p2 = ex2(y1.x), p3 = ex2(y1.y);
-          l0 += p0 + p2;
-          l1 += p1 + p3;
-          p[k >> 1] = pack_f16x2(p0 * s4.x, p1 * s4.y);
-          p[(k >> 1) + 1] = pack_f16x2(p2 * s4.z, p3 * s4.w);
+          const float2 p0 = make_float2(ex2(y0.x), ex2(y0.y)), p1 = make_float2(ex2(y1.x), ex2(y1.y));
+          sum = add2(sum, add2(p0, p1));
+          const float2 w0 = mul2(p0, make_float2(s4.x, s4.y)), w1 = mul2(p1, make_float2(s4.z, s4.w));
+          p[k >> 1] = pack_f16x2(w0.x, w0.y);
+          p[(k >> 1) + 1] = pack_f16x2(w1.x, w1.y);
         }
-        tmem_st16(s_at + 16u * c, p);
+        tmem_st16(s_at + 32u * c, p);
+        tmem_st16(s_at + 32u * c + 16u, p + 16);
       }
-      l += l0 + l1;
+      l += sum.x + sum.y;
       tmem_wait_st();
       tc::tc_fence_before();
       tc::mbar_arrive(&S.pfull[w]);
@@ -388,29 +419,31 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
     const int c = t - 256, cw = warp - 8;
     const int32_t *trow = a.table + (int64_t)b * a.cols;
     const int pmask = (1 << a.page_shift) - 1;
-    auto load = [&](int i, Slot &x) {
+    // the page of the thread's slot in tile i, looked up one load ahead: -1 for none
+    auto page_at = [&](int i) {
+      if (i >= tiles) return -1;
+      const int j = start_of(i) + c;
+      return j <= last_pos ? load_ahead(trow + (j >> a.page_shift)) : -1;
+    };
+    int page = page_at(0);
+    auto load = [&](int i, Slot &x) {  // tiles in order
       if (i >= tiles) return;
       const int j = start_of(i) + c;
-      int id = -1;
-      if (j <= last_pos) {
-        id = __ldg(trow + (j >> a.page_shift));
-        if ((unsigned)id >= (unsigned)a.num_pages) id = -1;
-      }
+      int id = (unsigned)page < (unsigned)a.num_pages ? page : -1;
+      page = page_at(i + 1);
       // a slot that no row sees may hold anything: keep it out
       x.has = id >= 0 && (a.window == 0 || j > first_pos - a.window || j < a.sinks);
       if (!x.has) id = 0;
       const int64_t row = (((int64_t)id * a.hkv + h) << a.page_shift) + (j & pmask);
-      const uint4 *k = reinterpret_cast<const uint4 *>(a.kc + row * (kD / 2));
-      const uint4 *v = reinterpret_cast<const uint4 *>(a.vc + row * (kD / 2));
+      const uint8_t *k = a.kc + row * (kD / 2), *v = a.vc + row * (kD / 2);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        x.k[q] = __ldg(k + q);
-        x.v[q] = __ldg(v + q);
-      }
-      x.ks = a.ks[row];
-      x.kz = a.kz[row];
-      x.vs = a.vs[row];
-      x.vz = a.vz[row];
+      for (int q = 0; q < 4; ++q) x.k[q] = load16_ahead(k + 16 * q);
+      x.ks = load_half_ahead(a.ks + row);
+      x.kz = load_half_ahead(a.kz + row);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) x.v[q] = load16_ahead(v + 16 * q);
+      x.vs = load_half_ahead(a.vs + row);
+      x.vz = load_half_ahead(a.vz + row);
     };
     const __half zero = __float2half_rn(0.0f);
     auto convert = [&](int i, const Slot &x) -> bool {
@@ -480,13 +513,18 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
     }
   } else if (lane == 0 && tiles > 0) {
     // ================================================================ products
-    const uint32_t sQ = tc::smem_u32(smem + kOffQ), sK = tc::smem_u32(smem + kOffK), sV = tc::smem_u32(smem + kOffV);
+    // descriptors of the first step; a step adds its byte offset / 16 to the address field. (One
+    // thread issues 32 products of 32 cycles a tile: what it does between them counts.)
+    const uint64_t dq = tc::smem_desc(tc::smem_u32(smem + kOffQ), 16, 1024);
+    const uint64_t dk = tc::smem_desc(tc::smem_u32(smem + kOffK), 16, 1024);
+    const uint64_t dv = tc::smem_desc(tc::smem_u32(smem + kOffV), kTile * 128u, 1024);
     auto scores = [&](int w, int st) {  // S_w = Q_w K^T
+      const uint64_t qw = dq + (uint32_t)w * (kOperand >> 4), kw = dk + (uint32_t)st * (kOperand >> 4);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const uint32_t at = (uint32_t)(k >> 2) * (kTile * 128u) + (uint32_t)(k & 3) * 32u;
-        tc::umma_bf16(tmem + 128u * w, tc::smem_desc(sQ + w * kOperand + at, 16, 1024),
-                      tc::smem_desc(sK + st * kOperand + at, 16, 1024), idesc(false), k > 0 ? 1u : 0u);
+        constexpr uint32_t kAtom = kTile * 128u >> 4;
+        const uint32_t at = (uint32_t)(k >> 2) * kAtom + (uint32_t)(k & 3) * 2u;
+        tc::umma_bf16(tmem + 128u * w, qw + at, kw + at, idesc(false), k > 0 ? 1u : 0u);
       }
       tc::umma_commit(&S.sfull[w]);
     };
@@ -506,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
 #pragma unroll
         for (int k = 0; k < 8; ++k)  // O_w += P_w V, 16 slots a step
           umma_tmem_a(tmem + 256u + 128u * w, tmem + 128u * w + 8u * k,
-                      tc::smem_desc(sV + st * kOperand + (uint32_t)k * 16u * 128u, kTile * 128u, 1024), idesc(true),
+                      dv + (uint32_t)st * (kOperand >> 4) + (uint32_t)k * (16u * 128u >> 4), idesc(true),
                       (i > 0 || k > 0) ? 1u : 0u);
         tc::umma_commit(&S.pvdone[w]);
         if (w == halves - 1) tc::umma_commit(&S.vempty[st]);

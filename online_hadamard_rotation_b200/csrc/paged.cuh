@@ -75,6 +75,25 @@ __device__ __forceinline__ float2 fma2(float2 x, float f, float c) {
   return r;
 }
 
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  uint64_t X, Y, R;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(X) : "f"(x.x), "f"(x.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(Y) : "f"(y.x), "f"(y.y));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(R) : "l"(X), "l"(Y));
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(R));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+  uint64_t X, Y, R;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(X) : "f"(x.x), "f"(x.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(Y) : "f"(y.x), "f"(y.y));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(R) : "l"(X), "l"(Y));
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(R));
+  return r;
+}
+
 // 16 consecutive TMEM columns of this thread's lane -> 16 registers
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t *r) {
   asm volatile(
