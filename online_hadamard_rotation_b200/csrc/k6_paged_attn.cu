@@ -235,6 +235,7 @@ struct alignas(16) Smem {
   long long before[kThreads], cut[kWarps + 1], base[kWarps];
   int seq[kWarps];
   Piece piece[kWarps][2];
+  float factor[2 * kWarps][R], top[2 * kWarps][R], den[2 * kWarps][R];
   alignas(16) float head[kWarps][R][kPart];
 };
 
@@ -667,36 +668,26 @@ struct Worker {
     }
   }
 
-  // Join pieces first .. last (in warp order, two places a warp) of one item, all threads.
-  __device__ void join(int first, int last, bool whole, float *out_part) {
+  // Join a group's pieces of one item (bits of `group`, in warp order) with their rows' factors, all
+  // threads: to out if the item is whole, else as a piece of the block's.
+  __device__ void join(uint32_t group, int first, bool whole, float *out_part) {
     const Piece &p = sm.piece[first >> 1][first & 1];
     const Seq s = load_seq(a, p.seq);
     for (int i = threadIdx.x; i < p.rows * (kD / 4); i += kThreads) {
       const int row = i / (kD / 4), e = 4 * (i % (kD / 4));
-      float top = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < 2 * kWarps; ++k)
-        if (k >= first && k <= last && sm.piece[k >> 1][k & 1].rows > 0)
-          top = fmaxf(top, piece_row(k >> 1, k & 1, row)[kD]);
-      float den = 0.0f;
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-      for (int k = 0; k < 2 * kWarps; ++k) {
-        const float *part = piece_row(k >> 1, k & 1, row);
-        if (k < first || k > last || sm.piece[k >> 1][k & 1].rows == 0 || part[kD] == -INFINITY) continue;
-        const float f = ex2(part[kD] - top);
-        const float4 x = *reinterpret_cast<const float4 *>(part + e);
-        den = fmaf(part[kD + 1], f, den);
+      for (uint32_t left = group; left; left &= left - 1) {
+        const int k = __ffs((int)left) - 1;
+        const float f = sm.factor[k][row];
+        const float4 x = *reinterpret_cast<const float4 *>(piece_row(k >> 1, k & 1, row) + e);
         v.x = fmaf(x.x, f, v.x);
         v.y = fmaf(x.y, f, v.y);
         v.z = fmaf(x.z, f, v.z);
         v.w = fmaf(x.w, f, v.w);
       }
       if (whole) {
-        const float inv = top == -INFINITY ? 0.0f : 1.0f / den;
         const int rr = p.tile * R + row, tok = rr / a.group;
         const int64_t at = ((int64_t)(s.q0 + tok) * a.hq + p.head * a.group + (rr - tok * a.group)) * kD + e;
-        v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
         if constexpr (F32)
           *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = v;
         else
@@ -705,8 +696,8 @@ struct Worker {
       } else {
         *reinterpret_cast<float4 *>(out_part + row * kPart + e) = v;
         if (e == 0) {
-          out_part[row * kPart + kD] = top;
-          out_part[row * kPart + kD + 1] = den;
+          out_part[row * kPart + kD] = sm.top[first][row];
+          out_part[row * kPart + kD + 1] = sm.den[first][row];
         }
       }
     }
@@ -824,22 +815,54 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k6_paged_attn(const
     }
   }
   __syncthreads();
-  // ---- join what the block's warps share; what reaches other blocks goes to the workspace
-  int4 rec = make_int4(0, 0, 0, 0);
-  for (int k = 0; k < 2 * kWarps;) {
-    if (sm.piece[k >> 1][k & 1].rows == 0) {
-      ++k;
-      continue;
+  // ---- join what the block's warps share; what reaches other blocks goes to the workspace. A group
+  // is the pieces of one item: it begins where the piece before it (in warp order) ended one.
+  uint32_t have = 0u, ended = 0u;
+#pragma unroll
+  for (int k = 0; k < 2 * kWarps; ++k) {
+    if (sm.piece[k >> 1][k & 1].rows > 0) have |= 1u << k;
+    if (sm.piece[k >> 1][k & 1].ends) ended |= 1u << k;
+  }
+  ended &= have;
+  auto group_of = [&](int k) -> uint32_t {  // pieces of piece k's item
+    const uint32_t before = ended & ((1u << k) - 1u), after = ended >> k;
+    const int lo = before ? 32 - __clz((int)before) : 0;       // behind the last end before k
+    const int hi = after ? k + __ffs((int)after) - 1 : 2 * kWarps - 1;  // the first end from k on
+    return have & ((2u << hi) - 1u) & ~((1u << lo) - 1u);
+  };
+  // factors of the pieces' rows in their item's sum, and the item's maximum and sum of weights
+  for (int i = t; i < 2 * kWarps * R; i += kThreads) {
+    const int k = i / R, row = i % R;
+    if (!(have >> k & 1u)) continue;
+    const uint32_t group = group_of(k);
+    float top = -INFINITY, den = 0.0f;
+    for (uint32_t left = group; left; left &= left - 1) {
+      const int j = __ffs((int)left) - 1;
+      top = fmaxf(top, w.piece_row(j >> 1, j & 1, row)[kD]);
     }
-    int last = k, j = k;  // up to the piece that ends the item, or the block's last
-    while (!sm.piece[last >> 1][last & 1].ends && ++j < 2 * kWarps)
-      if (sm.piece[j >> 1][j & 1].rows > 0) last = j;
-    const Piece p = sm.piece[k >> 1][k & 1];
-    const bool ends = sm.piece[last >> 1][last & 1].ends, whole = p.begins && ends;
+    for (uint32_t left = group; left; left &= left - 1) {
+      const int j = __ffs((int)left) - 1;
+      const float *part = w.piece_row(j >> 1, j & 1, row);
+      if (part[kD] != -INFINITY) den = fmaf(part[kD + 1], ex2(part[kD] - top), den);
+    }
+    const int first = __ffs((int)group) - 1;
+    const bool whole = sm.piece[first >> 1][first & 1].begins && (ended & group);
+    const float mine = w.piece_row(k >> 1, k & 1, row)[kD];
+    sm.factor[k][row] = mine == -INFINITY ? 0.0f : ex2(mine - top) * (whole ? 1.0f / den : 1.0f);
+    sm.top[k][row] = top;
+    sm.den[k][row] = den;
+  }
+  __syncthreads();
+  int4 rec = make_int4(0, 0, 0, 0);
+  for (uint32_t left = have; left;) {
+    const int first = __ffs((int)left) - 1;
+    const uint32_t group = group_of(first);
+    left &= ~group;
+    const Piece p = sm.piece[first >> 1][first & 1];
+    const bool ends = (ended & group) != 0u;
     // places in the workspace: 0 for an item begun by an earlier block, 1 for one begun here
-    w.join(k, last, whole, a.parts + ((int64_t)blockIdx.x * 2 + (p.begins ? 1 : 0)) * R * kPart);
+    w.join(group, first, p.begins && ends, a.parts + ((int64_t)blockIdx.x * 2 + (p.begins ? 1 : 0)) * R * kPart);
     if (p.begins && !ends) rec = make_int4(p.blocks, p.seq, p.head, p.tile);
-    k = last + 1;
   }
   if (t == 0 && !a.cuts.whole) a.recs[blockIdx.x] = rec;  // a call of short items has no workspace
 }
