@@ -415,20 +415,30 @@ struct Worker {
 
       // ---- scores: sc[n][t][..] = (slot of row g: rows 2c, 2c + 1; of row g + 8: the same)
       float sc[NT][MT][4];
+      // all of a thread's key codes first, then k steps with one product per tile: MT sums are under
+      // way at a time
+      uint4 kx[MT], ky[MT];
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         const uint8_t *key = st.keys + g * Stage<MT>::kKeyRun + 2 * t * 64 + 16 * c;
-        const uint4 kx = *reinterpret_cast<const uint4 *>(key), ky = *reinterpret_cast<const uint4 *>(key + 64);
-        const uint32_t wx[4] = {kx.x, kx.y, kx.z, kx.w}, wy[4] = {ky.x, ky.y, ky.z, ky.w};
+        kx[t] = *reinterpret_cast<const uint4 *>(key);
+        ky[t] = *reinterpret_cast<const uint4 *>(key + 64);
+      }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {  // k steps of 16 elements
-          const uint32_t x = (u & 1) ? wx[u >> 1] >> 8 : wx[u >> 1], v = (u & 1) ? wy[u >> 1] >> 8 : wy[u >> 1];
+      for (int u = 0; u < 8; ++u) {  // k steps of 16 elements
+        uint2 qf[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) qf[n] = sm.qfrag[warp][n][u][lane];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          const uint32_t wx = (u >> 1) == 0 ? kx[t].x : (u >> 1) == 1 ? kx[t].y : (u >> 1) == 2 ? kx[t].z : kx[t].w;
+          const uint32_t wy = (u >> 1) == 0 ? ky[t].x : (u >> 1) == 1 ? ky[t].y : (u >> 1) == 2 ? ky[t].z : ky[t].w;
+          const uint32_t x = (u & 1) ? wx >> 8 : wx, v = (u & 1) ? wy >> 8 : wy;
           const uint32_t a0 = x & 0x000F000Fu, a1 = v & 0x000F000Fu, a2 = x & 0x00F000F0u, a3 = v & 0x00F000F0u;
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const uint2 qf = sm.qfrag[warp][n][u][lane];
-            if (u == 0) mma_f16_first(sc[n][t], a0, a1, a2, a3, qf.x, qf.y);
-            else mma_f16(sc[n][t], a0, a1, a2, a3, qf.x, qf.y);
+            if (u == 0) mma_f16_first(sc[n][t], a0, a1, a2, a3, qf[n].x, qf[n].y);
+            else mma_f16(sc[n][t], a0, a1, a2, a3, qf[n].x, qf[n].y);
           }
         }
       }
