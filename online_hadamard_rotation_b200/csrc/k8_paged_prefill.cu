@@ -22,6 +22,15 @@
 // TMEM: S_0, S_1, O_0, O_1 of 128 columns each, all 512.
 // Every wait is bounded by a clock budget; on expiry the block records a status (read by
 // spin_device_status), stops, waits for its products and frees TMEM.
+//
+// Measured, 3 sequences of up to 4096 slots with 1027 to 2048 new tokens, 32 query and 8 kv heads:
+// 306 us, 637 TFLOP/s (four products' flops per visible slot). No unit is full there (tensor cores
+// and exponentials a third each, ALU 36 %, issue under half); leaving out the exponentials gives
+// 3 %, seven eighths of the products 8 %, three quarters of the expansion 11 %, half of the second
+// pass over the scores 14 %. Slower or no better on the same work: weights as a shared-memory
+// operand with the next scores issued before the value products (311 against 311 then), the same
+// with 16 softmax warps of 16 rows (316) and 8 converters (321), scores held in registers between
+// the passes (330 and more).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -60,16 +69,16 @@ struct Shared {
   alignas(16) float vs[2][kTile];  // value scales of a stage's slots (0 for those no row sees)
   float kscale[2], vexp[2];    // 2^e of the keys; exponent above the largest value scale
   uint32_t seen[2][4];         // slots of the stage that have a page and lie before the last row
-  uint32_t kmax[4], vmax[4];   // converters' warps
+  uint32_t kmax[2][4], vmax[2][4];  // converters' warps
 };
 constexpr uint32_t kSmemBytes = kOffS + sizeof(Shared) + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory per block");
 
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Shared &S, bool honor_abort = true) {
-  if (tc::mbar_try_wait_suspend(bar, parity)) return true;
+  if (tc::mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (true) {
-    if (tc::mbar_try_wait_suspend(bar, parity)) return true;
+    if (tc::mbar_try_wait(bar, parity)) return true;
     if (honor_abort && *reinterpret_cast<volatile int *>(&S.abort)) return false;
     if (clock64() - t0 > kTimeoutCycles) {
       *reinterpret_cast<volatile int *>(&S.abort) = 1;
@@ -81,6 +90,20 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Shared &S, 
 // The same for a warp whose lanes go on together.
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Shared &S) {
   return __all_sync(0xFFFFFFFFu, wait(bar, parity, S));
+}
+
+// Barrier of a group of warps that all go on or all leave: whether every thread came with ok.
+__device__ __forceinline__ bool named_and(uint32_t id, uint32_t threads, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"((uint32_t)ok)
+      : "memory");
+  return r != 0u;
 }
 
 // kind::f16 with fp16 operands, fp32 sums, M = N = 128; B K-major or MN-major.
@@ -446,6 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
       x.vz = load_half_ahead(a.vz + row);
     };
     const __half zero = __float2half_rn(0.0f);
+    bool ok = true;  // a warp whose wait ran out writes no more; all leave at the next barrier
     auto convert = [&](int i, const Slot &x) -> bool {
       const int st = i & 1;
       const uint32_t ph = (uint32_t)(i >> 1) & 1u;
@@ -454,16 +478,15 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
       const uint32_t kb = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(ks)));
       const uint32_t vb = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(vs)));
       const uint32_t has = __ballot_sync(0xFFFFFFFFu, x.has);
-      tc::named_sync(1, 128);  // the tile before has read kmax and vmax
-      if (lane == 0) {
-        S.kmax[cw] = kb;
-        S.vmax[cw] = vb;
+      if (lane == 0) {  // by the tile's parity: the tile before may still be read
+        S.kmax[st][cw] = kb;
+        S.vmax[st][cw] = vb;
       }
-      tc::named_sync(1, 128);
-      const uint32_t kt = max(max(S.kmax[0], S.kmax[1]), max(S.kmax[2], S.kmax[3]));
-      const uint32_t vt = max(max(S.vmax[0], S.vmax[1]), max(S.vmax[2], S.vmax[3]));
+      if (!named_and(1, 128, ok)) return false;
+      const uint32_t kt = max(max(S.kmax[st][0], S.kmax[st][1]), max(S.kmax[st][2], S.kmax[st][3]));
+      const uint32_t vt = max(max(S.vmax[st][0], S.vmax[st][1]), max(S.vmax[st][2], S.vmax[st][3]));
       const int ke = max((int)(kt >> 23) - 126, -24), ve = max((int)(vt >> 23) - 126, -24);
-      if (i >= 2 && !wait_warp(&S.kempty[st], ph ^ 1u, S)) return false;
+      if (i >= 2 && !(ok = wait_warp(&S.kempty[st], ph ^ 1u, S))) return true;
       {
         const uint32_t z = twice(x.has ? __float2half_rn(__half2float(x.kz) * (-1.0f / 512.0f)) : zero);
         const uint32_t mul = twice(__float2half_rn(ks * __int_as_float((127 + 9 - ke) << 23)));
@@ -481,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
         tc::fence_proxy_async_smem();
         tc::mbar_arrive(&S.kfull[st]);
       }
-      if (i >= 2 && !wait_warp(&S.vempty[st], ph ^ 1u, S)) return false;
+      if (i >= 2 && !(ok = wait_warp(&S.vempty[st], ph ^ 1u, S))) return true;
       {
         const uint32_t z = twice(x.has ? __float2half_rn(__half2float(x.vz) * (-1.0f / 512.0f)) : zero);
         uint8_t *dst = smem + kOffV + st * kOperand;
