@@ -430,13 +430,14 @@ typedef struct spin_kv_pages_t {
  *  out          [tokens, n_q_heads, head_dim] bf16 or fp32 (out_dtype), 16-byte aligned
  *  workspace    caller-owned device scratch of at least
  *               spin_paged_attention_workspace_bytes(n_q_heads, n_kv_heads, max_q_len,
- *               table_cols * page_size) bytes (may be NULL where that is 0), 16-byte aligned, contents on entry do not matter; calls (and captured graphs)
- *               that may run at the same time need separate workspaces
+ *               table_cols * page_size) bytes (may be NULL where that is 0), 16-byte aligned,
+ *               contents on entry do not matter; calls (and captured graphs) that may run at
+ *               the same time need separate workspaces
  * block_table, lens and cu_q are read on the device: a captured graph may be replayed after
  * their contents (not their sizes) change. seqs == 0 or tokens == 0 is a no-op.
  * Errors: SPIN_ERR_INVALID_ARG (null pointer, negative size, tokens != seqs without cu_q,
  * softmax_scale, out_dtype, workspace too small), SPIN_ERR_UNSUPPORTED_SIZE (head_dim,
- * page_size, head counts, tokens), SPIN_ERR_MISALIGNED, SPIN_ERR_DEVICE, SPIN_ERR_CUDA.
+ * page_size, head counts, tokens, seqs above 2^30), SPIN_ERR_MISALIGNED, SPIN_ERR_DEVICE, SPIN_ERR_CUDA.
  */
 spin_status_t spin_paged_attention_int4kv(const void *q, int32_t tokens, const spin_kv_pages_t *cache,
                                           const int32_t *block_table, int32_t seqs, int32_t table_cols,
@@ -458,8 +459,8 @@ size_t spin_paged_attention_workspace_bytes(int32_t n_q_heads, int32_t n_kv_head
  * several pairs; a page that is the destination of two pairs, or source and destination in one
  * call, ends with unspecified contents (no other page is affected).
  *  src_pages, dst_pages  [n] int32 in device memory; n >= 0 (0 is a no-op)
- * Errors: SPIN_ERR_INVALID_ARG, SPIN_ERR_UNSUPPORTED_SIZE (head_dim, geometries that differ),
- * SPIN_ERR_MISALIGNED, SPIN_ERR_DEVICE, SPIN_ERR_CUDA.
+ * Errors: SPIN_ERR_INVALID_ARG, SPIN_ERR_UNSUPPORTED_SIZE (head_dim, geometries that differ,
+ * n * n_kv_heads * page_size above 2^38), SPIN_ERR_MISALIGNED, SPIN_ERR_DEVICE, SPIN_ERR_CUDA.
  */
 spin_status_t spin_kv_pages_copy(const spin_kv_pages_t *src, const int32_t *src_pages, const spin_kv_pages_t *dst,
                                  const int32_t *dst_pages, int32_t n, spin_stream_t stream);
@@ -478,7 +479,7 @@ spin_status_t spin_kv_pages_copy(const spin_kv_pages_t *src, const int32_t *src_
  *             [cu_keep[0], cu_keep[rows]) are not used
  *  dst_start  [rows] int32 or NULL (0)
  *  src, dst agree in n_kv_heads and head_dim; page sizes are free
- * Errors: as spin_kv_pages_copy.
+ * Errors: as spin_kv_pages_copy, the limit being rows <= 2^30.
  */
 spin_status_t spin_kv_slots_copy(const spin_kv_pages_t *src, const int32_t *src_table, int32_t src_cols,
                                  const int32_t *keep, const int32_t *cu_keep, int32_t n, int32_t rows,
@@ -490,7 +491,8 @@ spin_status_t spin_kv_slots_copy(const spin_kv_pages_t *src, const int32_t *src_
  * and a stack of the pages nobody holds (the top is free_pages[*free_count - 1]). The three
  * calls below change it on `stream`; calls on one pool must be ordered (one stream, or events).
  * Rows and pages are taken in a fixed order, so the results repeat. A row that cannot be served
- * is left as it was and says so in `status`: nothing is half done.
+ * is left as it was and says so in `status`: nothing is half done. More than 2^30 rows or list
+ * entries are SPIN_ERR_UNSUPPORTED_SIZE.
  */
 typedef struct spin_kv_pool_t {
   int32_t *refs;       /* [pages] rows that hold the page, 0 for a free one */
@@ -520,9 +522,9 @@ spin_status_t spin_kv_pages_reserve(const spin_kv_pages_t *cache, const spin_kv_
  * Fork sequences: row children[i] becomes a second holder of row parents[i]'s full pages
  * (refs + 1) and gets the filled slots of its last, partly filled page in a page of its own,
  * popped from the stack and copied, so that both rows can be written on; its other columns
- * become -1, its length is the parent's. All parents are read as they were before the call. The child row must be empty
- * (length 0); of several forks into one row the first counts. Forks are served in order, as rows
- * in spin_kv_pages_reserve.
+ * become -1, its length is the parent's. All parents are read as they were before the call. The
+ * child row must be empty (length 0); of several forks into one row the first counts. Forks are
+ * served in order, as rows in spin_kv_pages_reserve.
  *  parents, children, status  [n] int32; block_table [rows, table_cols]; lens [rows]
  */
 spin_status_t spin_kv_pages_fork(const spin_kv_pages_t *cache, const spin_kv_pool_t *pool, int32_t *block_table,

@@ -139,6 +139,9 @@ static spin_status_t check_pages_memory(const spin_kv_pages_t *c) {
     return SPIN_ERR_MISALIGNED;
   return SPIN_OK;
 }
+// Rows, sequences and list entries a call may name: the kernels' int counters step past the last.
+constexpr int32_t kMostRows = 1 << 30;
+
 static KvPages kv_pages(const spin_kv_pages_t *c) {
   return KvPages{c->k_cache, c->v_cache, c->k_scale, c->k_zero, c->v_scale, c->v_zero, c->pages, c->n_kv_heads,
                  c->page_size};
@@ -308,7 +311,7 @@ spin_status_t spin_paged_attention_int4kv(const void *q, int32_t tokens, const s
       !std::isfinite(softmax_scale) || window < 0 || sinks < 0 || (out_dtype != SPIN_BF16 && out_dtype != SPIN_F32))
     return SPIN_ERR_INVALID_ARG;
   const int page = cache->page_size;
-  if (page < 16 || page > 65536 || (page & (page - 1)) != 0 || n_q_heads > 65535 ||
+  if (page < 16 || page > 65536 || (page & (page - 1)) != 0 || n_q_heads > 65535 || seqs > kMostRows ||
       (int64_t)tokens * n_q_heads >= (int64_t(1) << 31) ||
       (int64_t)cache->pages * cache->n_kv_heads * page >= (int64_t(1) << 31))
     return SPIN_ERR_UNSUPPORTED_SIZE;
@@ -353,8 +356,8 @@ spin_status_t spin_kv_pages_copy(const spin_kv_pages_t *src, const int32_t *src_
   if (!src_pages || !dst_pages) return SPIN_ERR_INVALID_ARG;
   if ((st = check_pages_memory(src)) != SPIN_OK || (st = check_pages_memory(dst)) != SPIN_OK) return st;
   if (!aligned(src_pages, 4) || !aligned(dst_pages, 4)) return SPIN_ERR_MISALIGNED;
-  // the grid's x limit, at 2048 pieces of 16 bytes a block
-  if ((int64_t)n * src->n_kv_heads * src->page_size > (int64_t(1) << 40)) return SPIN_ERR_UNSUPPORTED_SIZE;
+  // the grid's x limit, at 2048 pieces of 16 bytes a block and 8.5 pieces a row
+  if ((int64_t)n * src->n_kv_heads * src->page_size > (int64_t(1) << 38)) return SPIN_ERR_UNSUPPORTED_SIZE;
   if ((st = check_device()) != SPIN_OK) return st;
   return cuda_status(launch_kv_pages_copy(kv_pages(src), src_pages, kv_pages(dst), dst_pages, n,
                                           reinterpret_cast<cudaStream_t>(stream)));
@@ -369,6 +372,7 @@ spin_status_t spin_kv_slots_copy(const spin_kv_pages_t *src, const int32_t *src_
   if (st != SPIN_OK) return st;
   if (src->n_kv_heads != dst->n_kv_heads) return SPIN_ERR_UNSUPPORTED_SIZE;
   if (n < 0 || rows < 0 || src_cols < 1 || dst_cols < 1) return SPIN_ERR_INVALID_ARG;
+  if (rows > kMostRows) return SPIN_ERR_UNSUPPORTED_SIZE;
   if (n == 0 || rows == 0) return SPIN_OK;
   if (!src_table || !dst_table || !keep || !cu_keep) return SPIN_ERR_INVALID_ARG;
   if ((st = check_pages_memory(src)) != SPIN_OK || (st = check_pages_memory(dst)) != SPIN_OK) return st;
@@ -386,6 +390,7 @@ spin_status_t spin_kv_pages_reserve(const spin_kv_pages_t *cache, const spin_kv_
   spin_status_t st = check_pages(cache);
   if (st != SPIN_OK) return st;
   if (rows < 0 || table_cols < 1) return SPIN_ERR_INVALID_ARG;
+  if (rows > kMostRows) return SPIN_ERR_UNSUPPORTED_SIZE;
   if (rows == 0) return SPIN_OK;
   if (!add || !status) return SPIN_ERR_INVALID_ARG;
   if ((st = check_pool(pool, block_table, lens)) != SPIN_OK) return st;
@@ -402,6 +407,7 @@ spin_status_t spin_kv_pages_fork(const spin_kv_pages_t *cache, const spin_kv_poo
   spin_status_t st = check_pages(cache);
   if (st != SPIN_OK) return st;
   if (rows < 0 || table_cols < 1 || n < 0) return SPIN_ERR_INVALID_ARG;
+  if (rows > kMostRows || n > kMostRows) return SPIN_ERR_UNSUPPORTED_SIZE;
   if (n == 0) return SPIN_OK;
   if (!parents || !children || !status) return SPIN_ERR_INVALID_ARG;
   if ((st = check_pool(pool, block_table, lens)) != SPIN_OK) return st;
@@ -419,6 +425,7 @@ spin_status_t spin_kv_pages_free(const spin_kv_pages_t *cache, const spin_kv_poo
   spin_status_t st = check_pages(cache);
   if (st != SPIN_OK) return st;
   if (rows < 0 || table_cols < 1 || n < 0) return SPIN_ERR_INVALID_ARG;
+  if (rows > kMostRows || n > kMostRows) return SPIN_ERR_UNSUPPORTED_SIZE;
   if (n == 0) return SPIN_OK;
   if (!list) return SPIN_ERR_INVALID_ARG;
   if ((st = check_pool(pool, block_table, lens)) != SPIN_OK) return st;

@@ -1010,8 +1010,8 @@ cudaError_t launch_paged_attention(const PagedAttention &p, cudaStream_t stream)
   a.scale_log2 = p.softmax_scale * 1.4426950408889634f;
   a.out = p.out;
   a.row_limit = INT_MAX;
-  // chunks of prompts go to the tensor-memory kernel, other sequences of the same call (if there
-  // can be any) stay here; fp32 results do too, whose weights want two terms
+  // chunks of prompts go to the tensor-memory kernel, other sequences of the same call stay here;
+  // fp32 results do too, whose weights want two terms
   if (!p.out_f32 && (int64_t)p.max_q_len * a.group > kNarrowRows &&
       paged_prefill_worth(a.tokens, a.group, a.hkv)) {
     a.row_limit = kNarrowRows;

@@ -62,6 +62,20 @@ def test_attention_rules(L):
     assert attn(L, pages(k_scale=FAKE + 2)) == MIS and attn(L, pages(v_cache=FAKE + 8)) == MIS
 
 
+def test_limits_of_counts(L):
+    """What a kernel's grid and int counters cannot hold is refused before the device is asked."""
+    big, most = 1 << 30, (1 << 31) - 1
+    small = pages(n_kv_heads=8, page_size=64)  # 2^31 - 1 pairs: 2^40 slot rows of 8.5 pieces, 2048 pieces a block
+    assert L.spin_kv_pages_copy(small, FAKE, small, FAKE, most, None) == SIZE
+    assert L.spin_kv_pages_copy(small, FAKE, small, FAKE, (1 << 29) + 1, None) == SIZE
+    assert attn(L, seqs=big + 1) == SIZE and attn(L, seqs=most) == SIZE
+    assert L.spin_kv_slots_copy(pages(), FAKE, 4, FAKE, FAKE, 9, big + 1, pages(), FAKE, 4, None, None) == SIZE
+    for rows, n in ((big + 1, 3), (4, big + 1), (most, most)):
+        assert L.spin_kv_pages_fork(pages(), pool(), FAKE, rows, 8, FAKE, FAKE, FAKE, n, FAKE, None) == SIZE
+        assert L.spin_kv_pages_free(pages(), pool(), FAKE, rows, 8, FAKE, FAKE, n, None) == SIZE
+    assert L.spin_kv_pages_reserve(pages(), pool(), FAKE, big + 1, 8, FAKE, FAKE, FAKE, None) == SIZE
+
+
 def test_workspace_bytes(L):
     f = L.spin_paged_attention_workspace_bytes
     n = 1 << 40
