@@ -65,7 +65,7 @@ def attention(q, cache, table, lens, cu, scale=None, window=0, sinks=0):
                 out[t, g * group:(g + 1) * group] = w @ v
                 size[t, g * group:(g + 1) * group] = w @ v.abs()
                 floor[t, g * group:(g + 1) * group] = vs[at, g].max() * (vu[at, g] - vz[at, g]).abs().sum(0)
-                terms = (rows_q.abs() @ ku[at, g].T + rows_q.sum(1).abs()[:, None] * kz[at, g].T) * ks[at, g].T * scale
+                terms = (rows_q.abs() @ ku[at, g].T + rows_q.sum(1).abs()[:, None] * kz[at, g].T.abs()) * ks[at, g].T * scale
                 score_size = max(score_size, float(terms.max()))
                 score_rms = max(score_rms, float((rows_q ** 2 @ (k ** 2).T).max()) ** 0.5 * scale)
     return out, size, score_size, floor, score_rms

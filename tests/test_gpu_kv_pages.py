@@ -267,3 +267,32 @@ def test_pool_calls_captured_and_replayed(spin_gpu):
         torch.cuda.synchronize()
         assert st.tolist() == [0, 0, 0] and lens.tolist() == [0, 0, 0]
         assert pool["free_count"].item() == 16 and sorted(pool["free_pages"].tolist()) == list(range(16))
+
+
+def test_copies_and_pool_calls_on_another_stream(spin_gpu):
+    """A stream argument, and the current stream where there is none: each call sees what was enqueued before it."""
+    spin = spin_gpu
+    for given in (True, False):
+        s = torch.cuda.Stream()
+        kw = dict(stream=s) if given else {}
+        cache, big = ref.random_pages(12, 2, 16, 5), torch.zeros(1 << 26, device="cuda")
+        pool = spin.alloc_kv_pages(8, 2, 16)
+        table, lens, add = torch.full((2, 4), -1, dtype=torch.int32, device="cuda"), ints([0, 0]), ints([0, 0])
+        src, dst = ints([0, 0]), ints([5, 7])
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                big.add_(1)  # what is read below is written well after the calls were made
+            src.copy_(ints([3, 1]))
+            add.copy_(ints([20, 33]))
+        if given:
+            st = spin.reserve_kv_pages(pool, table, lens, add, **kw)
+            spin.copy_kv_pages(cache, src, dst, **kw)
+        else:
+            with torch.cuda.stream(s):
+                st = spin.reserve_kv_pages(pool, table, lens, add)
+                spin.copy_kv_pages(cache, src, dst)
+        s.synchronize()
+        assert st.tolist() == [0, 0] and lens.tolist() == [20, 33] and pool["free_count"].item() == 3
+        for name, t in cache.items():
+            assert torch.equal(t[5], t[3]) and torch.equal(t[7], t[1]), name

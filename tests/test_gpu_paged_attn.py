@@ -194,6 +194,96 @@ def test_lengths_and_offsets_are_clamped(spin_gpu):
     assert torch.equal(out, a)
 
 
+def odd_zeros(q, cache, table, lens, cu, seed, **kw):
+    """Any fp16 zeros of -4 .. 20 in the cache, and what check_attention needs for them.
+
+    The narrow kernel splits a value (c - z) s into (c - y) s under the rounded weight, 0 <= c, y < 16, and
+    (y - z) s under the fp32 one, |y - z| < 35: its terms are below 50 s. The kernel for chunks rounds
+    c - z, |c - z| < 20, to fp16 (half a step, 2^-11, once more beside the weight's): 40 s. 80 s in the
+    place of |vhat| bounds both. Its keys (c - z) s are rounded twice, the root of two times the
+    deviation: 1.5 here."""
+    g = torch.Generator().manual_seed(seed)
+    for n in ("k_zero", "v_zero"):
+        cache[n] = (24 * torch.rand(cache[n].shape, generator=g) - 4).half().cuda()
+    out, _, s, _, s2 = ref.attention(q, cache, table, lens, cu, **kw)
+    wide = dict(cache, v_cache=torch.zeros_like(cache["v_cache"]), v_zero=torch.full_like(cache["v_zero"], -80))
+    _, size, _, floor, _ = ref.attention(q, wide, table, lens, cu, **kw)
+    return out, size, s, floor, 1.5 * s2
+
+
+@pytest.mark.parametrize("hq,hkv,nq,kw", [(32, 8, 1, {}), (32, 8, 5, dict(window=70, sinks=9)), (5, 5, 1, {})])
+def test_zeros_between_the_codes(spin_gpu, hq, hkv, nq, kw):
+    lens = [300, 77, 9]
+    q, cache, table, cu = make(lens, [nq] * 3, hq, hkv, 32, seed=41)
+    want = odd_zeros(q, cache, table, lens, cu, 42, **kw)
+    ref.check_attention(run(spin_gpu, q, cache, table, lens, cu, **kw), want)
+    ref.check_attention(run(spin_gpu, q, cache, table, lens, cu, out_dtype=torch.bfloat16, **kw), want, "bf16")
+
+
+def test_zeros_between_the_codes_in_chunks_of_prompts(spin_gpu):
+    lens, nq = [600, 333], [400, 222]
+    q, cache, table, cu = make(lens, nq, 32, 8, 64, seed=43)
+    want = odd_zeros(q, cache, table, lens, cu, 44)
+    ref.check_attention(run(spin_gpu, q, cache, table, lens, cu, out_dtype=torch.bfloat16), want, "prefill")
+
+
+def test_more_and_fewer_tokens_than_expected(spin_gpu):
+    """max_q_len chooses a kernel; whatever it says, every token is computed."""
+    lens, nq = [400, 90, 33], [300, 4, 1]
+    q, cache, table, cu = make(lens, nq, 32, 8, 32, seed=45)
+    want = ref.attention(q, cache, table, lens, cu)
+    for most in (1, 2, 17, 2 ** 31 - 1):
+        ref.check_attention(run(spin_gpu, q, cache, table, lens, cu, max_q_len=most), want)
+        ref.check_attention(run(spin_gpu, q, cache, table, lens, cu, max_q_len=most, out_dtype=torch.bfloat16), want,
+                            "prefill")
+    lens, nq = [1 + i % 40 for i in range(600)], [1] * 600  # enough rows for chunks, and none there
+    q, cache, table, cu = make(lens, nq, 32, 8, 16, seed=46)
+    got = run(spin_gpu, q, cache, table, lens, cu, max_q_len=100, out_dtype=torch.bfloat16)
+    ref.check_attention(got, ref.attention(q, cache, table, lens, cu), "bf16")
+
+
+def test_tensors_inside_larger_ones(spin_gpu):
+    """q and out that begin 16 bytes into their storage, and nothing written around out."""
+    lens, nq = [500, 260], [300, 260]
+    q, cache, table, cu = make(lens, nq, 32, 8, 32, seed=47)
+    want = run(spin_gpu, q, cache, table, lens, cu, out_dtype=torch.bfloat16)
+    q2 = torch.full((q.numel() + 16,), 3.0, dtype=torch.bfloat16, device="cuda")
+    q2[8:-8] = q.flatten()
+    o2 = torch.full_like(q2, -7.0)
+    got = run(spin_gpu, q2[8:-8].view(q.shape), cache, table, lens, cu, out=o2[8:-8].view(q.shape))
+    assert torch.equal(got, want) and (o2[:8] == -7).all() and (o2[-8:] == -7).all()
+
+
+def test_chunks_of_prompts_at_once_and_replayed(spin_gpu):
+    """Two calls on two streams at once, and a captured one replayed after the lengths changed."""
+    lens, nq = [900, 700], [400, 300]
+    q, cache, table, cu, want = prefill(spin_gpu, lens, nq, 32, 8, 64, seed=48)
+    one, many = make([3000], [1], 32, 8, 64, seed=49), [torch.cuda.Stream() for _ in range(2)]
+    single = run(spin_gpu, *one[:3], [3000], one[3])
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        for i, s in enumerate(many):
+            with torch.cuda.stream(s):
+                got.append(run(spin_gpu, q, cache, table, lens, cu, out_dtype=torch.bfloat16) if i == 0 else
+                           run(spin_gpu, *one[:3], [3000], one[3]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for x in got[::2]) and all(torch.equal(x, single) for x in got[1::2])
+    n, c = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (lens, cu))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = spin_gpu.paged_attention_int4kv(q, cache, table, n, c, 400, out_dtype=torch.bfloat16)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    lens = [650, 5]
+    n.copy_(torch.tensor(lens, dtype=torch.int32))
+    g.replay()
+    torch.cuda.synchronize()
+    ref.check_attention(out, ref.attention(q, cache, table, lens, cu), "prefill")
+    assert spin_gpu.device_status() == 0
+
+
 def test_rows_behind_the_last_sequence_stay(spin_gpu):
     lens, nq = [100, 33], [2, 3]
     q, cache, table, cu = make(lens, nq, 8, 2, 32, seed=8)
