@@ -10,11 +10,11 @@
 
 namespace spin {
 
-// How the narrow kernel cuts its work into runs: units an item costs besides its slot blocks, how
-// close to an item's end a cut moves to it, the shortest run worth a warp of its own, and whether
-// items are so short that each stays in one block of threads (no second kernel joins pieces then).
+// How the narrow kernel cuts its work into runs: units an item costs besides its slot blocks, and
+// whether items are so short that each stays in one block of threads (no second kernel joins pieces
+// then).
 struct Cuts {
-  int item, snap, min_run, whole;
+  int item, whole;
 };
 
 struct PagedArgs {
