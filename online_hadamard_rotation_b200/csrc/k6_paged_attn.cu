@@ -45,8 +45,8 @@
 // asynchronous copies that look up a page per 16 slots. The next keys are under way during the
 // softmax and the value products, the next values during the scores. Rows are padded in runs so
 // that all reads are free of bank conflicts; bulk copies of such runs (512 bytes) took 36 cycles
-// each on the copy engine and were slower. (Loads straight into registers, 32 slots a block at the same occupancy: 83 us
-// against 67 on 4 rows of up to 65537 slots, fp32.)
+// each on the copy engine and were slower. (Loads straight into registers, 32 slots a block at the
+// same occupancy: 83 us against 67 on 4 rows of up to 65537 slots, fp32.)
 // The softmax keeps one reference per row that is raised only when a weight could pass 2^14 (a
 // raised one leaves 2^9), so most blocks need no cross-lane maximum; fp16's smallest step is then
 // 2^-33 of the row's largest weight or less.
@@ -61,6 +61,19 @@
 // go to the workspace and a second kernel joins them in order. Every thread block derives the
 // cuts from lens and cu_q itself: the host reads nothing back, and no atomics are used, so
 // results repeat bit for bit.
+//
+// What bounds it: instructions. A block of 64 slots and 8 rows costs a warp about 1300 (expanding
+// 8 KB of codes, 64 products, the softmax of 16 numbers a lane); three warps a scheduler issue 0.65 a
+// cycle with the ALU, whose instructions take two cycles, at 40 %. Measured (8 kv heads, 4 query
+// heads each but for the drafts' 8):
+//   32 sequences of up to 4096 slots, one token        28.6 us, 2.6 TB/s (a copy's time: 11.2 us)
+//   4 sequences of 40001 to 65537 slots, fp32 results  61.4 us, 3.4 TB/s (32.1)
+//   16 sequences, four tokens, window 4096, 4 sinks    57.8 us, 1.2 TB/s (10.6); 32 rows a kv head are
+//                                                      two tiles, each expands the codes
+//   one sequence of 257 slots                          10 us: the latency of cuts, first loads, softmax
+//                                                      and join in a row
+// Blocks of threads with 3 instead of 2 to an SM (16-row tiles, 168 registers) take 61.4 us for the
+// drafts.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -81,10 +94,19 @@ constexpr int kD = 128;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCtas = 600;  // most blocks of a launch (sets the workspace)
-constexpr Cuts kCoarse = {2, 0};  // where every warp has several blocks
-constexpr Cuts kFine = {0, 0};    // where there are fewer blocks than warps: one each, latency counts
-constexpr int kWholeUnits = 16;  // items up to this length stay in one block of threads
-constexpr int kNarrowRows = 64;  // rows of a sequence (tokens x group) that are this kernel's in any call
+// An item's fixed cost (its queries, its piece) is that of two slot blocks (28.6 us for 32 sequences of
+// up to 4096 slots and 68.3 for 64 of up to 8192; at one block 27.9 and 73.4, at three 28.8 and 68.1).
+// Where there are fewer blocks than warps, a block each is best: 4 sequences of 1000 slots take
+// 11.2 us, 12.0 by the other rule.
+constexpr Cuts kCoarse = {2, 0};
+constexpr Cuts kFine = {0, 0};
+// Items of up to this many units stay in one block of threads, without a join: 32 sequences of 500
+// slots take 15.1 us, cut 15.7; one of 257 10.4 and 10.8; at 40 units one of 2000 takes 19.0, cut 11.5.
+constexpr int kWholeUnits = 16;
+// Rows of a sequence (tokens x group) that are this kernel's in any call: 40 sequences of 1024 slots
+// with 64 rows a kv head take 72.5 us here and 89.8 in the tensor-memory kernel, 30 with 80 rows
+// 68.8 and 62.9.
+constexpr int kNarrowRows = 64;
 constexpr int kPart = 132;     // floats per row of a piece: 128 sums, max, sum of weights, pad
 constexpr float kRoom = 9.0f;   // a raised reference leaves weights at most 2^kRoom
 constexpr float kRaise = 5.0f;  // log2 above that at which it is raised again (fp16 ends at 2^16)

@@ -601,8 +601,10 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
 }  // namespace
 
 bool paged_prefill_worth(int tokens, int group, int n_kv_heads) {
-  // below half a block per SM the finer cuts of the narrow kernel fill the GPU better
-  return (int64_t)n_kv_heads * tokens * group / kRows >= 74;
+  // below a quarter of a block per SM the finer cuts of the narrow kernel fill the GPU better: one
+  // sequence of 2048 slots, 8 kv heads of 4, with 150 new tokens (18 blocks) takes 38.9 us there and
+  // 57.6 here, with 300 (37 blocks) 64.5 and 58.5, with 592 103 and 58
+  return (int64_t)n_kv_heads * tokens * group / kRows >= 37;
 }
 
 cudaError_t launch_paged_prefill(const PagedArgs &a, cudaStream_t stream) {
