@@ -82,7 +82,7 @@ def test_windows_and_sinks(spin_gpu, window, sinks, nq):
 
 
 def prefill(spin, lens, nq, hq, hkv, page, seed, **kw):
-    """Calls with enough rows for the kernel for chunks of prompts (74 blocks of 256)."""
+    """Calls with enough rows for the kernel for chunks of prompts (37 blocks of 256 and more)."""
     assert hkv * sum(nq) * (hq // hkv) // 256 >= 74
     q, cache, table, cu = make(lens, nq, hq, hkv, page, seed)
     want = ref.attention(q, cache, table, lens, cu, **kw)
