@@ -494,6 +494,14 @@ def _empty(shape, dtype, device: int, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _empty_like(t: torch.Tensor, dtype, stream) -> torch.Tensor:
+    """_empty with the shape and device of a (contiguous) argument: half the host time of naming them."""
+    if stream is None:
+        return torch.empty_like(t, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t, dtype=dtype)
+
+
 def _refuse(t: torch.Tensor, name: str, device: int, want: str) -> None:
     if t.dtype is not _I32:
         raise TypeError(f"{name}: expected torch.int32, got {t.dtype}")
@@ -607,7 +615,7 @@ def paged_attention_int4kv(q: torch.Tensor, cache: dict, block_table: torch.Tens
     if out_dtype is not torch.float32 and out_dtype is not torch.bfloat16:
         raise TypeError(f"out_dtype: expected torch.float32 or torch.bfloat16, got {out_dtype}")
     if out is None:
-        out = _empty((tokens, hq, d), out_dtype, device, stream)
+        out = _empty_like(q, out_dtype, stream)
     else:
         _rows(out, "out", out_dtype, device, (tokens, hq, d))
     ws_at = ws_bytes = 0
@@ -672,10 +680,10 @@ def copy_kv_slots(src: dict, src_table: torch.Tensor, keep: torch.Tensor, cu_kee
     return dst
 
 
-def _status(out, n: int, device: int, stream) -> torch.Tensor:
+def _status(out, like: torch.Tensor, device: int, stream) -> torch.Tensor:
     if out is None:
-        return _empty((n,), _I32, device, stream)
-    _vec(out, "status", device, n)
+        return _empty_like(like, _I32, stream)
+    _vec(out, "status", device, like.numel())
     return out
 
 
@@ -687,7 +695,7 @@ def reserve_kv_pages(pool: dict, block_table: torch.Tensor, lens: torch.Tensor, 
     KV_REFUSED (bad length or count, no column left)."""
     kv, p, device, table, n, cols, lens_at = _pool(pool, block_table, lens)
     add_at = _vec(add, "add", device, n)
-    status = _status(status, n, device, stream)
+    status = _status(status, add, device, stream)
     _call("spin_kv_pages_reserve", device, stream, kv, p, table, n, cols, lens_at, add_at, status.data_ptr())
     return status
 
@@ -702,7 +710,7 @@ def fork_kv_pages(pool: dict, block_table: torch.Tensor, lens: torch.Tensor, par
     n = parents.numel()
     parents_at = _vec(parents, "parents", device, n)
     children_at = _vec(children, "children", device, n)
-    status = _status(status, n, device, stream)
+    status = _status(status, parents, device, stream)
     _call("spin_kv_pages_fork", device, stream, kv, p, table, rows, cols, lens_at, parents_at, children_at, n,
           status.data_ptr())
     return status
