@@ -64,7 +64,7 @@
 //
 // What bounds it: instructions. A block of 64 slots and 8 rows costs a warp about 1300 (expanding
 // 8 KB of codes, 64 products, the softmax of 16 numbers a lane); three warps a scheduler issue 0.65 a
-// cycle with the ALU, whose instructions take two cycles, at 40 %. Measured (8 kv heads, 4 query
+// cycle while they run (0.46 over a launch of 28 us) with the ALU at 40 %. Measured (8 kv heads, 4 query
 // heads each but for the drafts' 8):
 //   32 sequences of up to 4096 slots, one token        28.6 us, 2.6 TB/s (a copy's time: 11.2 us)
 //   4 sequences of 40001 to 65537 slots, fp32 results  61.4 us, 3.4 TB/s (32.1)

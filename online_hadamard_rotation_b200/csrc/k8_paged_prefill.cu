@@ -24,13 +24,13 @@
 // spin_device_status), stops, waits for its products and frees TMEM.
 //
 // Measured, 3 sequences of up to 4096 slots with 1027 to 2048 new tokens, 32 query and 8 kv heads:
-// 306 us, 637 TFLOP/s (four products' flops per visible slot). No unit is full there (tensor cores
-// and exponentials a third each, ALU 36 %, issue under half); leaving out the exponentials gives
-// 3 %, seven eighths of the products 8 %, three quarters of the expansion 11 %, half of the second
-// pass over the scores 14 %. Slower or no better on the same work: weights as a shared-memory
-// operand with the next scores issued before the value products (311 against 311 then), the same
-// with 16 softmax warps of 16 rows (316) and 8 converters (321), scores held in registers between
-// the passes (330 and more).
+// 306 us, 637 TFLOP/s (four products' flops per visible slot). No unit is full there: tensor cores
+// and exponentials a third each, ALU 28 %, issue 38 %. No better on the same work: weights as a
+// shared-memory operand with the next scores issued before the value products (311 against 311
+// then), the same with 16 softmax warps of 16 rows (316) and 8 converters (321), scores held in
+// registers between the passes (330 and more). In the widest of these, leaving out the exponentials
+// gained 6 %, seven eighths of the products 11 %, three quarters of the expansion 11 %, half of the
+// second pass over the scores 15 %: the units wait for one another.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
