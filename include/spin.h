@@ -421,7 +421,7 @@ typedef struct spin_kv_pages_t {
  *  cache        pages as above; page_size a power of two, 16 .. 65536
  *  block_table  [seqs, table_cols] int32
  *  lens         [seqs] int32, slots of each sequence, the new tokens' among them; a value
- *               outside [0, table_cols * page_size] is clamped to it
+ *               outside [0, table_cols * page_size] (2^30 at most) is clamped to it
  *  cu_q         [seqs + 1] int32, token offsets (ascending, within [0, tokens], clamped to it);
  *               NULL: one token per sequence, tokens == seqs. Rows of out outside
  *               [cu_q[0], cu_q[seqs]) are left as they were.
