@@ -391,8 +391,8 @@ spin_status_t spin_decode_attention_int4kv_noalloc(const void *q, const uint8_t 
  * [batch, n_kv_heads, cache_len, ...] is `batch` pages of cache_len slots, so its writer and
  * the copies below work on either). A sequence's pages are named by its row of a block table
  * [rows, table_cols] int32: slot j of row b is slot j % page_size of page
- * table[b][j / page_size]. Table entries behind a row's last page are never used. An entry
- * outside [0, pages) has no memory behind it: operators that read it see no slot there, and
+ * table[b][j / page_size]. Attention and the copies never use the table entries behind a row's last
+ * page (the pool's calls below keep the pages of a row that was cut there). An entry outside [0, pages) has no memory behind it: operators that read it see no slot there, and
  * copies skip it. Page offsets are 64-bit throughout.
  */
 typedef struct spin_kv_pages_t {
@@ -496,6 +496,13 @@ spin_status_t spin_kv_slots_copy(const spin_kv_pages_t *src, const int32_t *src_
  * Rows and pages are taken in a fixed order, so the results repeat. A row that cannot be served
  * is left as it was and says so in `status`: nothing is half done. More than 2^30 rows or list
  * entries are SPIN_ERR_UNSUPPORTED_SIZE.
+ *
+ * A row may be cut between calls by lowering lens[b] to 1 or more (rejected drafts, say). It keeps
+ * the pages behind its new length, in the columns where they stand, up to the first column that
+ * names none: it grows over them again and gives them back with the others when it is let go. A
+ * row of length 0 holds nothing (let a row go with spin_kv_pages_free, not by its length). A row
+ * that grew from length 0 needs no particular contents of its columns beforehand; one whose
+ * columns and length were written by the caller has -1 behind its last page.
  */
 typedef struct spin_kv_pool_t {
   int32_t *refs;       /* [pages] rows that hold the page, 0 for a free one */
@@ -510,8 +517,8 @@ typedef struct spin_kv_pool_t {
 
 /*
  * Make room for add[b] more slots in every row b: pages are popped for the slots that no page
- * of the row holds yet (refs 1), their ids written to the row's next columns, and lens[b] grows
- * by add[b]. Rows are served in order: row b gets its pages if the pages wanted by rows 0 .. b
+ * of the row holds yet (refs 1), their ids written to the row's next columns and -1 behind them,
+ * and lens[b] grows by add[b]. Rows are served in order: row b gets its pages if the pages wanted by rows 0 .. b
  * together are free (refused rows want none); a row that wants none is always served. The last
  * page of a row that is partly filled is assumed to be the row's own, as after
  * spin_kv_pages_fork: cut a forked row no shorter than it was when forked.
@@ -535,8 +542,8 @@ spin_status_t spin_kv_pages_fork(const spin_kv_pages_t *cache, const spin_kv_poo
                                  const int32_t *children, int32_t n, int32_t *status, spin_stream_t stream);
 
 /*
- * Let rows go: each listed row gives up its pages (refs - 1), its columns become -1 and its
- * length 0; pages that nobody holds any more go on the free stack in ascending
+ * Let rows go: each listed row gives up its pages (refs - 1), those it kept when it was cut among
+ * them, its columns become -1 and its length 0; pages that nobody holds any more go on the free stack in ascending
  * order. A row that is empty, listed twice or outside [0, rows) gives up nothing (more).
  *  list  [n] int32
  */

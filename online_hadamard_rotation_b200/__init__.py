@@ -690,7 +690,8 @@ def _status(out, like: torch.Tensor, device: int, stream) -> torch.Tensor:
 def reserve_kv_pages(pool: dict, block_table: torch.Tensor, lens: torch.Tensor, add: torch.Tensor,
                      status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Room for add[b] more slots in every row: pages are popped from the pool (alloc_kv_pages)
-    into block_table [rows, cols] and lens [rows] grows, in row order. Returns int32 [rows]:
+    into block_table [rows, cols] and lens [rows] grows, in row order. A row whose length was lowered
+    since (to 1 or more: rejected drafts) kept its pages and grows over them first. Returns int32 [rows]:
     KV_OK, KV_NO_PAGES (the free pages do not reach this row, which is left as it was) or
     KV_REFUSED (bad length or count, no column left)."""
     kv, p, device, table, n, cols, lens_at = _pool(pool, block_table, lens)

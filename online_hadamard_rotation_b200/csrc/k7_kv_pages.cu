@@ -230,28 +230,38 @@ __device__ __forceinline__ int free_pages_of(const PoolArgs &a) { return min(max
 
 constexpr int kOwnWant = 4;  // a row that wants more pages than this is filled by a warp
 
-// One block: the pages wanted by each row, a prefix sum, then each served row's columns. A decode
-// step wants at most a page or two a row, which its thread writes itself; the long rows of a
-// prompt are left to whole warps (with warps for every row, 1280 rows took 30 us). The order of
-// rows decides who is served, so one block scans them all; it is bound by the latency of that
-// chain of loads: 1280 rows take 7 us.
+// Whether column col of a row names a page that this row alone holds.
+__device__ __forceinline__ bool own_page(const PoolArgs &a, int64_t row, int64_t col) {
+  const int id = a.table[row * a.cols + col];
+  return (unsigned)id < (unsigned)a.pages && a.refs[id] == 1;
+}
+
+// One block: the pages wanted by each row, a prefix sum, then each served row's columns. A row that
+// was cut keeps its pages in the columns behind its length, up to the first that names none: the
+// columns are counted first and no page is popped for them. (A row of length 0 holds nothing.) So
+// that what a table held before a row's first page is never taken for such pages, a row that gets
+// new ones gets -1 behind them. A decode step wants at most a page or two a row, which its thread
+// looks up and writes itself; the long rows of a prompt are left to whole warps (with warps for
+// every row, 1280 rows took 30 us). The order of rows decides who is served, so one block scans
+// them all; it is bound by the latency of that chain of loads: 1280 rows take 7 us.
 __global__ void __launch_bounds__(kPlanThreads)
     k7_reserve(const PoolArgs a, const int32_t *__restrict__ add, int32_t *__restrict__ status) {
   __shared__ long long sums[kPlanThreads / 32];
   __shared__ unsigned long long s_taken;
   __shared__ int s_long[kPlanThreads], s_longs;
   __shared__ long long s_depth[kPlanThreads];
-  __shared__ int s_want[kPlanThreads], s_have[kPlanThreads];
-  const int count = free_pages_of(a), t = threadIdx.x;
+  __shared__ int s_want[kPlanThreads], s_have[kPlanThreads], s_kept[kPlanThreads];
+  const int count = free_pages_of(a), t = threadIdx.x, lane = t & 31;
   if (t == 0) {
     s_taken = 0;
     s_longs = 0;
   }
+  __syncthreads();
   long long carry = 0;
   for (int b0 = 0; b0 < a.rows; b0 += kPlanThreads) {
     const int b = b0 + t;
     long long want = 0, have = 0;
-    int st = SPIN_KV_REFUSED, len = 0, n = 0;
+    int st = SPIN_KV_REFUSED, len = 0, n = 0, kept = 0, listed = -1;
     if (b < a.rows) {
       len = a.lens[b];
       n = add[b];
@@ -262,6 +272,40 @@ __global__ void __launch_bounds__(kPlanThreads)
       }
       if (st != SPIN_KV_OK) want = 0;
     }
+    auto list = [&]() {  // any order: each row's pages are fixed
+      const int k = atomicAdd(&s_longs, 1);
+      s_long[k] = b;
+      s_want[k] = (int)want;
+      s_have[k] = (int)have;
+      return k;
+    };
+    // ---- columns whose pages the row kept
+    if (want > 0 && len > 0) {
+      if (want <= kOwnWant) {
+        while (kept < want && own_page(a, b, have + kept)) ++kept;
+      } else {
+        listed = list();
+      }
+    }
+    __syncthreads();
+    for (int k = t >> 5; k < s_longs; k += kPlanThreads / 32) {
+      const int64_t row = s_long[k];
+      const int first = s_have[k], most = s_want[k];
+      int got = 0;
+      while (true) {
+        const bool own = got + lane < most && own_page(a, row, first + got + lane);
+        const unsigned other = ~__ballot_sync(0xFFFFFFFFu, own);
+        got += other ? __ffs((int)other) - 1 : 32;
+        if (other) break;
+      }
+      if (lane == 0) s_kept[k] = got;
+    }
+    __syncthreads();
+    if (listed >= 0) kept = s_kept[listed];
+    if (t == 0) s_longs = 0;
+    have += kept;
+    want -= kept;
+    // ---- who is served
     long long total;
     const long long upto = carry + block_scan(want, sums, total);
     carry += total;
@@ -273,32 +317,34 @@ __global__ void __launch_bounds__(kPlanThreads)
       status[b] = st;
       if (st == SPIN_KV_OK) a.lens[b] = len + n;
     }
+    // ---- columns of the served rows
     auto give = [&](int64_t row, int col, long long depth) {
       const int id = stack_page(a, count, depth);
       a.table[row * a.cols + col] = id;
       if (id >= 0) a.refs[id] = 1;
+    };
+    auto stop = [&](int64_t row, int col) {
+      if (col < a.cols) a.table[row * a.cols + col] = -1;
     };
     if (want > 0) {
       // served rows are the first of the prefix, so the largest one is what was taken
       atomicMax(&s_taken, (unsigned long long)upto);
       if (want <= kOwnWant) {
         for (int j = 0; j < (int)want; ++j) give(b, (int)have + j, upto - want + j);
+        stop(b, (int)(have + want));
       } else {
-        const int k = atomicAdd(&s_longs, 1);  // any order: each row's pages are fixed
-        s_long[k] = b;
-        s_depth[k] = upto - want;
-        s_want[k] = (int)want;
-        s_have[k] = (int)have;
+        s_depth[list()] = upto - want;
       }
     }
     __syncthreads();
-    const int longs = s_longs;
-    for (int k = t >> 5; k < longs; k += kPlanThreads / 32)
-      for (int j = t & 31; j < s_want[k]; j += 32) give(s_long[k], s_have[k] + j, s_depth[k] + j);
+    for (int k = t >> 5; k < s_longs; k += kPlanThreads / 32) {
+      for (int j = lane; j < s_want[k]; j += 32) give(s_long[k], s_have[k] + j, s_depth[k] + j);
+      if (lane == 0) stop(s_long[k], s_have[k] + s_want[k]);
+    }
     __syncthreads();
     if (t == 0) s_longs = 0;
+    __syncthreads();
   }
-  __syncthreads();
   if (t == 0 && s_taken > 0) *a.count = count - (int)s_taken;
 }
 
@@ -426,22 +472,33 @@ __global__ void __launch_bounds__(kForkThreads)
 constexpr int kFreeThreads = 128;
 
 // Free, first step: block i takes row list[i] (whoever takes its length first), empties its
-// columns and drops its pages. A page whose last holder left is marked by kFreed. Integer atomics:
+// columns and drops its pages, those among them that a cut left behind its length (up to the first
+// column that names none). A page whose last holder left is marked by kFreed. Integer atomics:
 // their order changes no result. 1024 rows take 8 us.
 __global__ void __launch_bounds__(kFreeThreads) k7_free_rows(const PoolArgs a, const int32_t *__restrict__ list) {
-  __shared__ int s_len;
+  __shared__ int s_len, s_end;
   tc::grid_dep_launch();
   const int r = list[blockIdx.x];
   if ((unsigned)r >= (unsigned)a.rows) return;
-  if (threadIdx.x == 0) s_len = atomicExch(a.lens + r, 0);
+  if (threadIdx.x == 0) {
+    s_len = atomicExch(a.lens + r, 0);
+    s_end = a.cols;
+  }
   __syncthreads();
   const int held = (int)min(((long long)s_len + a.page - 1) / a.page, (long long)a.cols);
   if (held <= 0) return;
   int32_t *row = a.table + (int64_t)r * a.cols;
+  for (int64_t j0 = held; j0 < a.cols; j0 += kFreeThreads) {
+    const int64_t j = j0 + threadIdx.x;
+    const bool none = j < a.cols && (unsigned)row[j] >= (unsigned)a.pages;
+    if (none) atomicMin(&s_end, (int)j);
+    if (__syncthreads_or(none)) break;
+  }
+  const int end = s_end;
   for (int j = threadIdx.x; j < a.cols; j += kFreeThreads) {
     const int id = row[j];
     row[j] = -1;
-    if (j >= held || (unsigned)id >= (unsigned)a.pages) continue;
+    if (j >= end || (unsigned)id >= (unsigned)a.pages) continue;
     const int old = atomicSub(a.refs + id, 1);
     if (old == 1) atomicMin(a.refs + id, kFreed);
     else if (old <= 0) atomicAdd(a.refs + id, 1);  // a page that nobody held: its count stays
