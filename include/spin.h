@@ -513,15 +513,15 @@ typedef struct spin_kv_pool_t {
 /* Values of `status`, per row or fork. */
 #define SPIN_KV_OK 0       /* done */
 #define SPIN_KV_NO_PAGES 1 /* not enough free pages */
-#define SPIN_KV_REFUSED 2  /* a bad index, length or count, a child that is not empty, no column left */
+#define SPIN_KV_REFUSED 2  /* a bad index, length or count, a child that is not empty, no column left, a shared page */
 
 /*
  * Make room for add[b] more slots in every row b: pages are popped for the slots that no page
  * of the row holds yet (refs 1), their ids written to the row's next columns and -1 behind them,
  * and lens[b] grows by add[b]. Rows are served in order: row b gets its pages if the pages wanted by rows 0 .. b
- * together are free (refused rows want none); a row that wants none is always served. The last
- * page of a row that is partly filled is assumed to be the row's own, as after
- * spin_kv_pages_fork: cut a forked row no shorter than it was when forked.
+ * together are free (refused rows want none); a row that wants none is always served. A row never
+ * grows onto a page that other rows hold too: a forked one that was cut shorter than it was when
+ * forked is SPIN_KV_REFUSED as long as they do.
  *  block_table [rows, table_cols], lens [rows], add [rows], status [rows]: int32
  */
 spin_status_t spin_kv_pages_reserve(const spin_kv_pages_t *cache, const spin_kv_pool_t *pool, int32_t *block_table,

@@ -693,7 +693,8 @@ def reserve_kv_pages(pool: dict, block_table: torch.Tensor, lens: torch.Tensor, 
     into block_table [rows, cols] and lens [rows] grows, in row order. A row whose length was lowered
     since (to 1 or more: rejected drafts) kept its pages and grows over them first. Returns int32 [rows]:
     KV_OK, KV_NO_PAGES (the free pages do not reach this row, which is left as it was) or
-    KV_REFUSED (bad length or count, no column left)."""
+    KV_REFUSED (bad length or count, no column left, or the row would grow onto a page that other
+    rows hold too: forked, then cut shorter than it was)."""
     kv, p, device, table, n, cols, lens_at = _pool(pool, block_table, lens)
     add_at = _vec(add, "add", device, n)
     status = _status(status, add, device, stream)

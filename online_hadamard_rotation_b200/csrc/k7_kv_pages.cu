@@ -230,17 +230,19 @@ __device__ __forceinline__ int free_pages_of(const PoolArgs &a) { return min(max
 
 constexpr int kOwnWant = 4;  // a row that wants more pages than this is filled by a warp
 
-// Whether column col of a row names a page that this row alone holds.
-__device__ __forceinline__ bool own_page(const PoolArgs &a, int64_t row, int64_t col) {
+// How many rows hold the page that column col of a row names; 0 if it names none.
+__device__ __forceinline__ int holders(const PoolArgs &a, int64_t row, int64_t col) {
   const int id = a.table[row * a.cols + col];
-  return (unsigned)id < (unsigned)a.pages && a.refs[id] == 1;
+  return (unsigned)id < (unsigned)a.pages ? a.refs[id] : 0;
 }
 
 // One block: the pages wanted by each row, a prefix sum, then each served row's columns. A row that
 // was cut keeps its pages in the columns behind its length, up to the first that names none: the
 // columns are counted first and no page is popped for them. (A row of length 0 holds nothing.) So
 // that what a table held before a row's first page is never taken for such pages, a row that gets
-// new ones gets -1 behind them. A decode step wants at most a page or two a row, which its thread
+// new ones gets -1 behind them. A row that would write on a page which other rows hold too (a forked
+// one cut shorter than it was then) is refused: its last, partly filled page and the first column
+// that it did not keep alone are looked at. A decode step wants at most a page or two a row, which its thread
 // looks up and writes itself; the long rows of a prompt are left to whole warps (with warps for
 // every row, 1280 rows took 30 us). The order of rows decides who is served, so one block scans
 // them all; it is bound by the latency of that chain of loads: 1280 rows take 7 us.
@@ -251,6 +253,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   __shared__ int s_long[kPlanThreads], s_longs;
   __shared__ long long s_depth[kPlanThreads];
   __shared__ int s_want[kPlanThreads], s_have[kPlanThreads], s_kept[kPlanThreads];
+  __shared__ bool s_shared[kPlanThreads];
   const int count = free_pages_of(a), t = threadIdx.x, lane = t & 31;
   if (t == 0) {
     s_taken = 0;
@@ -280,9 +283,12 @@ __global__ void __launch_bounds__(kPlanThreads)
       return k;
     };
     // ---- columns whose pages the row kept
+    bool shared = st == SPIN_KV_OK && n > 0 && len % a.page != 0 && holders(a, b, len / a.page) > 1;
     if (want > 0 && len > 0) {
       if (want <= kOwnWant) {
-        while (kept < want && own_page(a, b, have + kept)) ++kept;
+        int h = 0;
+        while (kept < want && (h = holders(a, b, have + kept)) == 1) ++kept;
+        shared |= h > 1;
       } else {
         listed = list();
       }
@@ -293,18 +299,29 @@ __global__ void __launch_bounds__(kPlanThreads)
       const int first = s_have[k], most = s_want[k];
       int got = 0;
       while (true) {
-        const bool own = got + lane < most && own_page(a, row, first + got + lane);
-        const unsigned other = ~__ballot_sync(0xFFFFFFFFu, own);
+        const int h = got + lane < most ? holders(a, row, first + got + lane) : 0;
+        const unsigned other = ~__ballot_sync(0xFFFFFFFFu, h == 1);
         got += other ? __ffs((int)other) - 1 : 32;
-        if (other) break;
+        if (!other) continue;
+        if (lane == __ffs((int)other) - 1) {
+          s_kept[k] = got;
+          s_shared[k] = h > 1;
+        }
+        break;
       }
-      if (lane == 0) s_kept[k] = got;
     }
     __syncthreads();
-    if (listed >= 0) kept = s_kept[listed];
+    if (listed >= 0) {
+      kept = s_kept[listed];
+      shared |= s_shared[listed];
+    }
     if (t == 0) s_longs = 0;
     have += kept;
     want -= kept;
+    if (shared) {
+      st = SPIN_KV_REFUSED;
+      want = 0;
+    }
     // ---- who is served
     long long total;
     const long long upto = carry + block_scan(want, sums, total);

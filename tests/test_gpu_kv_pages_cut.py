@@ -26,8 +26,12 @@ class Pool(ref.Pool):
                 status.append(2)
                 continue
             have, total = -(-length // self.page), -(-(length + n) // self.page)
+            shared = n > 0 and length % self.page and self.holders(row[have - 1]) > 1
             while length > 0 and have < total and self.holders(row[have]) == 1:
                 have += 1
+            if shared or (length > 0 and have < total and self.holders(row[have]) > 1):
+                status.append(2)
+                continue
             asked += total - have
             if total > have and asked > free:
                 status.append(1)
@@ -157,3 +161,26 @@ def test_captured_draft_steps(spin_gpu):
     assert pool["free_count"].item() == 2
     spin.free_kv_pages(pool, table, lens, ints([0, 1]))
     assert pool["free_count"].item() == 12 and (pool["refs"] == 0).all()
+
+
+@pytest.mark.parametrize("far", [0, 200])
+def test_no_row_grows_onto_a_shared_page(spin_gpu, far):
+    """Forked rows cut into the pages they share: refused while others hold these, at a page's end and
+    inside it, for a few slots and for many (`far`); served once the row alone holds them."""
+    b = Cut(spin_gpu, pages=60, hkv=1, page=16, rows=4, cols=20)
+    b.reserve([100, 0, 0, 40])
+    b.fork([0, 0], [1, 2])
+    b.cut({0: 32, 1: 33, 2: 95})
+    b.reserve([far + 1, 0, 0, 0])            # the next column names a shared page
+    b.reserve([0, far + 15, far + 1, 4])     # the last page is shared
+    b.reserve([0, 0, 0, 0])                  # nothing wanted, nothing refused
+    assert b.lens.tolist() == [32, 33, 95, 44]
+    b.free([0])
+    b.reserve([5, far + 1, 0, 0])            # still shared by the two children
+    b.free([1])
+    b.reserve([0, 7, far + 2, 0])
+    assert b.lens.tolist() == [5, 7, 97 + far, 44]
+    b.cut({2: 20})
+    b.reserve([0, 0, far + 60, 0])
+    b.free([0, 1, 2, 3])
+    b.everything_back()
