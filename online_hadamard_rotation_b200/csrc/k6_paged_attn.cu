@@ -678,7 +678,8 @@ struct Worker {
 #pragma unroll
           for (int t = 0; t < 4; ++t) reinterpret_cast<float4 *>(dst + 16 * g)[t] = v[t];
           if (g == 0) {
-            dst[kD] = m[n][r];
+            // a row of NaN scores never raised its reference: it must not look like one that saw no slot
+            dst[kD] = l[n][r] != l[n][r] ? 0.0f : m[n][r];
             dst[kD + 1] = l[n][r];
           }
         }

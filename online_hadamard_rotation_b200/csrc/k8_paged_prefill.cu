@@ -419,7 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
     if (ok && tiles > 0) ok = wait_warp(&S.pvdone[w], (uint32_t)(tiles - 1) & 1u, S);
     if (w < halves && ok) {
       tc::tc_fence_after();
-      const float inv = l > 0.0f ? kCode / l : 0.0f;
+      const bool none = l == 0.0f;  // no slot seen; a NaN among the scores made l NaN
+      const float inv = kCode / l;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t x[32];
@@ -431,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + qrow + 32 * c);
 #pragma unroll
         for (int k = 0; k < 32; k += 8) {
-          auto v = [&](int e) { return m == -INFINITY ? 0.0f : __uint_as_float(x[k + e]) * inv; };
+          auto v = [&](int e) { return none ? 0.0f : __uint_as_float(x[k + e]) * inv; };
           dst[k >> 3] = make_uint4(pack_bf16x2(v(0), v(2)), pack_bf16x2(v(4), v(6)), pack_bf16x2(v(1), v(3)),
                                    pack_bf16x2(v(5), v(7)));
         }
