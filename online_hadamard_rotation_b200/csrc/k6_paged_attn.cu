@@ -436,6 +436,11 @@ struct Worker {
       HalfVec<S> hks, hkz;
       hks.load(&st.steps[0][S * g]);
       hkz.load(&st.steps[1][S * g]);
+#pragma unroll
+      for (int k = 0; k < S / 2; ++k) {  // what is not finite becomes NaN, and so the slot's scores
+        hks.v[k] = fma_f16x2(hks.v[k], 0u, hks.v[k]);
+        hkz.v[k] = fma_f16x2(hkz.v[k], 0u, hkz.v[k]);
+      }
 
       // ---- scores: sc[n][t][..] = (slot of row g: rows 2c, 2c + 1; of row g + 8: the same)
       float sc[NT][MT][4];

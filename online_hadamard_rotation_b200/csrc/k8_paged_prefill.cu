@@ -8,11 +8,15 @@
 //
 // A block of threads takes 256 rows of one kv head (64 tokens at 4 query heads per kv head) and
 // walks the visible slots 128 at a time. The codes are expanded once for all 256 rows:
-//   keys    (c - z) s 2^-e in fp16, e the exponent above the tile's largest s (one rounding, 2^-12)
-//   values  (c - z) 2^-9, exact for whole zeros; their scales go into the weights
+//   (c - z) 2^-9, exact for whole zeros (0 .. 15, as R3 writes them); the keys' scales multiply the
+//   scores, the values' the weights, so no key scale reaches another slot or a row that does not see
+//   it. (In the keys' operand they cost a rounding of each key, whose errors add up where a query
+//   follows a key, and what the scales have in common; the call measured below took 312 us so, and
+//   339 with the scores' 128 shared-memory reads and the look at the bound.)
 // as K-major and MN-major operands with the 128-byte swizzle (eight codes of a word come out in
 // the order 0, 4, 1, 5, 2, 6, 3, 7; the queries are packed alike and the output is put back).
-// Queries are scaled by a power of two per row, as in k6, so they are exact in fp16.
+// Queries are scaled by a power of two, one for the block where its rows allow it (the keys' scales
+// then carry all that a score lacks), so they are exact in fp16.
 //   warps 0-3, 4-7  softmax of rows 0-127 and 128-255: a thread owns a row (a TMEM lane), reads its
 //                   scores, writes the weights p s' as fp16 over them (the A operand of the value
 //                   product stays in TMEM), and rescales its sums only when its reference moves
@@ -57,7 +61,7 @@ constexpr uint32_t kOperand = kTile * kD * 2;  // bytes of a 128 x 128 fp16 oper
 constexpr uint32_t kOffQ = 0, kOffK = 2 * kOperand, kOffV = 4 * kOperand, kOffS = 6 * kOperand;
 constexpr float kRoom = 9.0f;   // a raised reference leaves weights at most 2^kRoom
 constexpr float kRaise = 5.0f;  // log2 above that at which it is raised again (fp16 ends at 2^16)
-constexpr float kCode = 512.0f; // what the value codes' 2^-9 takes out
+constexpr float kCode = 512.0f; // what the codes' 2^-9 takes out
 constexpr long long kTimeoutCycles = 4000000000LL;  // about two seconds
 
 struct Shared {
@@ -66,10 +70,12 @@ struct Shared {
   int abort;
   int seq, pair;               // the block's item
   int sums[kThreads / 32], total;
-  alignas(16) float vs[2][kTile];  // value scales of a stage's slots (0 for those no row sees)
-  float kscale[2], vexp[2];    // 2^e of the keys; exponent above the largest value scale
+  alignas(16) float ks[2][kTile], vs[2][kTile];  // scales of a stage's slots (1, 0 for those no row sees)
+  float vexp[2], kmin[2], kmax[2];  // exponent above the largest value scale; ends of the key scales
+  float kmul;                  // what a key scale is multiplied by: the queries' 2^(E - 14), the softmax scale
+  uint32_t qtop[8];            // largest exponents of the queries, by warp
   uint32_t seen[2][4];         // slots of the stage that have a page and lie before the last row
-  uint32_t kmax[2][4], vmax[2][4];  // converters' warps
+  uint32_t wvmax[2][4], wkmin[2][4], wkmax[2][4];  // the same of the converters' warps
 };
 constexpr uint32_t kSmemBytes = kOffS + sizeof(Shared) + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory per block");
@@ -135,11 +141,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
-  return r;
-}
 __device__ __forceinline__ uint32_t fma_f16x2(uint32_t x, uint32_t y, uint32_t z) {
   uint32_t r;
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(z));
@@ -151,12 +152,11 @@ __device__ __forceinline__ uint32_t twice(__half h) {
 }
 
 // Eight codes as (u - z) 2^-9, from zero = -z 2^-9: a nibble under a mask is the subnormal u 2^-24
-// or u 2^-20.
-__device__ __forceinline__ uint4 codes8(uint32_t w, uint32_t zero) {
-  const uint32_t v = w >> 8;
-  return make_uint4(
-      fma_f16x2(w & 0x000F000Fu, 0x78007800u, zero), fma_f16x2(w & 0x00F000F0u, 0x68006800u, zero),
-      fma_f16x2(v & 0x000F000Fu, 0x78007800u, zero), fma_f16x2(v & 0x00F000F0u, 0x68006800u, zero));
+// or u 2^-20. sign (of both halves) and a zero of the other sign make (z - u) 2^-9.
+__device__ __forceinline__ uint4 codes8(uint32_t w, uint32_t zero, uint32_t sign = 0u) {
+  const uint32_t v = w >> 8, lo = 0x78007800u | sign, hi = 0x68006800u | sign;
+  return make_uint4(fma_f16x2(w & 0x000F000Fu, lo, zero), fma_f16x2(w & 0x00F000F0u, hi, zero),
+                    fma_f16x2(v & 0x000F000Fu, lo, zero), fma_f16x2(v & 0x00F000F0u, hi, zero));
 }
 
 // Byte offset of 16-byte piece j (eight elements) of row r of an operand: two atoms of 64 elements,
@@ -182,13 +182,26 @@ __device__ __forceinline__ int load_ahead(const int32_t *p) {
   return v;
 }
 
-// Scores of hidden slots (bits of v0, v1 that are not set) become -inf.
-__device__ __forceinline__ void hide(uint32_t (&x)[64], uint32_t v0, uint32_t v1) {
+// 64 scores times their slots' key scales.
+__device__ __forceinline__ void scale_keys(uint32_t (&x)[64], const float *ks) {
 #pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    x[k] = (v0 >> k & 1u) ? x[k] : 0xFF800000u;
-    x[32 + k] = (v1 >> k & 1u) ? x[32 + k] : 0xFF800000u;
+  for (int k = 0; k < 64; k += 4) {
+    const float4 s = *reinterpret_cast<const float4 *>(ks + k);
+    const float2 a = mul2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), make_float2(s.x, s.y));
+    const float2 b = mul2(make_float2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])), make_float2(s.z, s.w));
+    x[k] = __float_as_uint(a.x), x[k + 1] = __float_as_uint(a.y);
+    x[k + 2] = __float_as_uint(b.x), x[k + 3] = __float_as_uint(b.y);
   }
+}
+
+__device__ __forceinline__ float largest(const uint32_t (&x)[64]) {  // NaN among them do not count
+  float a = __uint_as_float(x[0]), b = __uint_as_float(x[1]);
+#pragma unroll
+  for (int k = 2; k < 62; k += 4) {
+    a = max3(a, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+    b = max3(b, __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
+  }
+  return max3(fmaxf(a, b), __uint_as_float(x[62]), __uint_as_float(x[63]));
 }
 
 struct Slot {  // what a converter holds of its slot of a tile
@@ -291,9 +304,10 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
     const int hi_pos = s.len - s.nq + (rr0 + min(128 * w + 127, rows - 1)) / a.group;
     const uint32_t s_at = tmem + 128u * w + ((uint32_t)(warp & 3) << 21);        // lane quarter in bits 16+
     const uint32_t o_at = tmem + 256u + 128u * w + ((uint32_t)(warp & 3) << 21);
-    float qmul;
+    float own;  // what a row's scores lack beside the keys' scales: 1, or a power of two
     {
-      // the row's largest exponent, then its values times 2^(14 - e) in fp16
+      // The row's largest exponent e and the block's, E; then its values times 2^(14 - E) in fp16,
+      // exact down to 2^-31 of the block's largest. Rows more than 2^8 below that take 2^(14 - e).
       const uint4 *src = reinterpret_cast<const uint4 *>(a.q + qrow);
       uint32_t top = 0u;
 #pragma unroll 4
@@ -304,8 +318,16 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
         for (int k = 0; k < 4; ++k) top = max(top, max(v[k] & 0x7FFFu, (v[k] >> 16) & 0x7FFFu));
       }
       const int e = min(max((int)(top >> 7) - 127, -100), 126);
-      const float up = __int_as_float((min(14 - e, 126) + 127) << 23);
-      qmul = __int_as_float((127 - min(14 - e, 126)) << 23) * a.scale_log2;
+      const uint32_t wtop = __reduce_max_sync(0xFFFFFFFFu, top < 0x7F80u ? (uint32_t)(e + 128) : 0u);
+      if (lane == 0) S.qtop[warp] = wtop;
+      tc::named_sync(2, 256);
+      uint32_t btop = 0u;
+      for (int k = 0; k < 8; ++k) btop = max(btop, S.qtop[k]);
+      const int E = min(max((int)btop - 128, -40), 60);
+      const int er = top == 0u || (e <= E && e >= E - 8) ? E : e;
+      const float up = __int_as_float((14 - er + 127) << 23);
+      own = __int_as_float((max(er - E, -126) + 127) << 23);
+      if (t == 0) S.kmul = __int_as_float((127 + E - 14) << 23) * kCode * a.scale_log2;
       uint8_t *qs = smem + kOffQ + w * kOperand;
 #pragma unroll 4
       for (int j = 0; j < 16; ++j) {
@@ -317,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
       tc::fence_proxy_async_smem();
       tc::mbar_arrive(&S.qfull);
     }
+    const bool owns = __any_sync(0xFFFFFFFFu, own != 1.0f);
     float m = -INFINITY, l = 0.0f;
     bool ok = w < halves;
     for (int i = 0; ok && i < tiles; ++i) {
@@ -326,7 +349,6 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
       if (!(ok = wait_warp(&S.vfull[st], ph, S))) break;
       tc::tc_fence_after();
       const int j0 = start_of(i);
-      const float f = qmul * S.kscale[st];
       const float vexp = S.vexp[st];
       const uint32_t *seen = S.seen[st];
       const bool all_seen = (seen[0] & seen[1] & seen[2] & seen[3]) == 0xFFFFFFFFu && j0 + kTile - 1 <= lo_pos &&
@@ -342,8 +364,28 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
         if (a.window > 0) v &= ~below(pos - a.window + 1) | below(a.sinks);
         return v & seen[c];
       };
-      // ---- the row's largest score (its scores are read twice: 128 registers for them would spill,
-      // and what spills is read back through an L1 that shared memory leaves small)
+      // ---- scores of hidden slots become -inf in their place, and a row's own factor goes in; most
+      // tiles need neither
+      if (owns || !all_seen) {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t x[32];
+          tc::tmem_ld32(s_at + 32u * c, x);
+          tc::tmem_wait_ld();
+          const uint32_t v = visible(c);
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            x[k] = (v >> k & 1u) ? __float_as_uint(__uint_as_float(x[k]) * own) : 0xFF800000u;
+          tmem_st16(s_at + 32u * c, x);
+          tmem_st16(s_at + 32u * c + 16u, x + 16);
+        }
+        tmem_wait_st();
+      }
+      // ---- can a weight exceed the row's reference by too much? The largest raw score times the ends
+      // of the tile's key scales bounds the scores; where that is not enough (the first tile, large
+      // scores), the scores are read once more and scaled one by one. (Every row reads its scores
+      // twice or more: 128 registers for them would spill, and what spills is read back through an L1
+      // that shared memory leaves small.)
       float top = -INFINITY;
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
@@ -351,17 +393,23 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
         tc::tmem_ld32(s_at + 64u * c, x);
         tc::tmem_ld32(s_at + 64u * c + 32u, x + 32);
         tc::tmem_wait_ld();
-        if (!all_seen) hide(x, visible(2 * c), visible(2 * c + 1));
-        float t0 = __uint_as_float(x[0]), t1 = __uint_as_float(x[1]);
-#pragma unroll
-        for (int k = 2; k < 62; k += 4) {
-          t0 = max3(t0, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-          t1 = max3(t1, __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
-        }
-        t0 = max3(t0, __uint_as_float(x[62]), __uint_as_float(x[63]));
-        top = max3(top, t0, t1);
+        top = fmaxf(top, largest(x));
       }
-      top = fmaf(top, f, vexp);
+      if (top != -INFINITY) top = fmaxf(top * S.kmin[st], top * S.kmax[st]);
+      top += vexp;
+      if (__any_sync(0xFFFFFFFFu, !(top <= m + kRoom + kRaise))) {
+        top = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          uint32_t x[64];
+          tc::tmem_ld32(s_at + 64u * c, x);
+          tc::tmem_ld32(s_at + 64u * c + 32u, x + 32);
+          tc::tmem_wait_ld();
+          scale_keys(x, &S.ks[st][64 * c]);
+          top = fmaxf(top, largest(x));
+        }
+        top += vexp;
+      }
       // ---- raise the reference where a weight could exceed it by too much
       const bool raise = top > m + kRoom + kRaise;  // false while both are -inf
       if (__any_sync(0xFFFFFFFFu, raise)) {
@@ -393,14 +441,14 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
         uint32_t x[64], p[32];
         tc::tmem_ld32(s_at + 64u * c, x);
         tc::tmem_ld32(s_at + 64u * c + 32u, x + 32);
+        const float4 *ks = reinterpret_cast<const float4 *>(&S.ks[st][64 * c]);
         const float4 *vs = reinterpret_cast<const float4 *>(&S.vs[st][64 * c]);
         tc::tmem_wait_ld();
-        if (!all_seen) hide(x, visible(2 * c), visible(2 * c + 1));
 #pragma unroll
         for (int k = 0; k < 64; k += 4) {
-          const float4 s4 = vs[k >> 2];
-          const float2 y0 = fma2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), f, -mr);
-          const float2 y1 = fma2(make_float2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])), f, -mr);
+          const float4 k4 = ks[k >> 2], s4 = vs[k >> 2];
+          const float2 y0 = fma2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), make_float2(k4.x, k4.y), -mr);
+          const float2 y1 = fma2(make_float2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])), make_float2(k4.z, k4.w), -mr);
           const float2 p0 = make_float2(ex2(y0.x), ex2(y0.y)), p1 = make_float2(ex2(y1.x), ex2(y1.y));
           sum = add2(sum, add2(p0, p1));
           const float2 w0 = mul2(p0, make_float2(s4.x, s4.y)), w1 = mul2(p1, make_float2(s4.z, s4.w));
@@ -470,42 +518,53 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
       x.vz = load_half_ahead(a.vz + row);
     };
     const __half zero = __float2half_rn(0.0f);
-    bool ok = true;  // a warp whose wait ran out writes no more; all leave at the next barrier
+    // a warp whose wait ran out writes no more; all leave at the next barrier
+    bool ok = true;
+    float kmul = 0.0f;
     auto convert = [&](int i, const Slot &x) -> bool {
       const int st = i & 1;
       const uint32_t ph = (uint32_t)(i >> 1) & 1u;
-      // exponents above the tile's largest scales
-      const float ks = x.has ? __half2float(x.ks) : 0.0f, vs = x.has ? __half2float(x.vs) : 0.0f;
-      const uint32_t kb = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(ks)));
+      // The scale a score meets is finite and above 0, so that it leaves the -inf of a hidden slot what
+      // it is: its sign is the key's, a scale of 0 becomes 2^-120, and where scale or zero is not
+      // finite the key is NaN.
+      const float kraw = __half2float(x.ks), kzero = __half2float(x.kz);
+      const bool sound = isfinite(kraw) && isfinite(kzero);
+      const float ks = x.has && sound ? fabsf(kraw) : 1.0f;
+      const float vs = x.has ? __half2float(x.vs) : 0.0f;
+      // over the tile's slots: the exponent above the largest value scale, the ends of the key scales
       const uint32_t vb = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(vs)));
+      const uint32_t kn = __reduce_min_sync(0xFFFFFFFFu, x.has ? __float_as_uint(ks) : 0x7F800000u);
+      const uint32_t kx = __reduce_max_sync(0xFFFFFFFFu, x.has ? __float_as_uint(ks) : 0u);
       const uint32_t has = __ballot_sync(0xFFFFFFFFu, x.has);
       if (lane == 0) {  // by the tile's parity: the tile before may still be read
-        S.kmax[st][cw] = kb;
-        S.vmax[st][cw] = vb;
+        S.wvmax[st][cw] = vb;
+        S.wkmin[st][cw] = kn;
+        S.wkmax[st][cw] = kx;
       }
       if (!named_and(1, 128, ok)) return false;
-      const uint32_t kt = max(max(S.kmax[st][0], S.kmax[st][1]), max(S.kmax[st][2], S.kmax[st][3]));
-      const uint32_t vt = max(max(S.vmax[st][0], S.vmax[st][1]), max(S.vmax[st][2], S.vmax[st][3]));
-      const int ke = max((int)(kt >> 23) - 126, -24), ve = max((int)(vt >> 23) - 126, -24);
+      auto over = [&](auto f, const uint32_t (&w)[4]) { return f(f(w[0], w[1]), f(w[2], w[3])); };
+      auto most = [](uint32_t x, uint32_t y) { return max(x, y); };
+      auto least = [](uint32_t x, uint32_t y) { return min(x, y); };
       if (i >= 2 && !(ok = wait_warp(&S.kempty[st], ph ^ 1u, S))) return true;
       {
-        const uint32_t z = twice(x.has ? __float2half_rn(__half2float(x.kz) * (-1.0f / 512.0f)) : zero);
-        const uint32_t mul = twice(__float2half_rn(ks * __int_as_float((127 + 9 - ke) << 23)));
+        const uint32_t sign = kraw < 0.0f ? 0x80008000u : 0u;
+        const float shift = kzero * (kraw < 0.0f ? 1.0f / 512.0f : -1.0f / 512.0f);
+        const uint32_t z = twice(!x.has ? zero : __float2half_rn(sound ? shift : NAN));
         uint8_t *dst = smem + kOffK + st * kOperand;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const uint32_t word[4] = {x.k[q].x, x.k[q].y, x.k[q].z, x.k[q].w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint4 y = codes8(word[e], z);
-            *reinterpret_cast<uint4 *>(dst + piece_at(c, 4 * q + e)) =
-                make_uint4(mul_f16x2(y.x, mul), mul_f16x2(y.y, mul), mul_f16x2(y.z, mul), mul_f16x2(y.w, mul));
-          }
+          for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4 *>(dst + piece_at(c, 4 * q + e)) = codes8(word[e], z, sign);
         }
         tc::fence_proxy_async_smem();
         tc::mbar_arrive(&S.kfull[st]);
       }
       if (i >= 2 && !(ok = wait_warp(&S.vempty[st], ph ^ 1u, S))) return true;
+      if (i == 0) {
+        if (!(ok = wait_warp(&S.qfull, 0, S))) return true;
+        kmul = S.kmul;
+      }
       {
         const uint32_t z = twice(x.has ? __float2half_rn(__half2float(x.vz) * (-1.0f / 512.0f)) : zero);
         uint8_t *dst = smem + kOffV + st * kOperand;
@@ -515,11 +574,13 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
 #pragma unroll
           for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4 *>(dst + piece_at(c, 4 * q + e)) = codes8(word[e], z);
         }
+        S.ks[st][c] = fmaxf(ks * kmul, 0x1p-120f);
         S.vs[st][c] = vs;
         if (lane == 0) S.seen[st][cw] = has;
         if (c == 0) {
-          S.kscale[st] = __int_as_float((127 + ke) << 23);
-          S.vexp[st] = (float)ve;
+          S.vexp[st] = (float)max((int)(over(most, S.wvmax[st]) >> 23) - 126, -24);
+          S.kmin[st] = fmaxf(__uint_as_float(over(least, S.wkmin[st])) * kmul, 0x1p-120f);
+          S.kmax[st] = fmaxf(__uint_as_float(over(most, S.wkmax[st])) * kmul, 0x1p-120f);
         }
         tc::fence_proxy_async_smem();
         tc::mbar_arrive(&S.vfull[st]);

@@ -64,10 +64,10 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 }
 
 // {x * f + c}, both lanes
-__device__ __forceinline__ float2 fma2(float2 x, float f, float c) {
+__device__ __forceinline__ float2 fma2(float2 x, float2 f, float c) {
   uint64_t X, F, C, R;
   asm("mov.b64 %0, {%1, %2};" : "=l"(X) : "f"(x.x), "f"(x.y));
-  asm("mov.b64 %0, {%1, %1};" : "=l"(F) : "f"(f));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(F) : "f"(f.x), "f"(f.y));
   asm("mov.b64 %0, {%1, %1};" : "=l"(C) : "f"(c));
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(R) : "l"(X), "l"(F), "l"(C));
   float2 r;

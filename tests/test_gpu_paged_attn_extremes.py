@@ -50,3 +50,105 @@ def test_nan_queries_give_nan(spin_gpu, shape, dtype):
     got = torch.where(fine[..., None].cuda(), got, want[0].to(got.dtype).cuda())
     what = "" if dtype == F32 else "prefill" if shape.startswith("chunk") else "bf16"
     ref.check_attention(got, want, what)
+
+
+def sees(lens, nq, slot, window=0, sinks=0):
+    """Which tokens of the first sequence see its slot `slot`, as a mask over all tokens."""
+    p = torch.arange(lens[0] - nq[0], lens[0])
+    m = torch.zeros(sum(nq), dtype=torch.bool)
+    m[:nq[0]] = (slot <= p) & ((p - slot < window) | (slot < sinks) if window else torch.ones_like(p, dtype=torch.bool))
+    return m
+
+
+def poison(cache, table, page, slot, **steps):
+    for name, value in steps.items():
+        cache[name][table[0, slot // page].item(), :, slot % page] = value
+
+
+# several tokens: tiles of 8 and 16 rows, chunks; a slot in the middle of the new ones; windows that leave it
+SOME = {"two heads": ([300, 40], [5, 1], 2, 2, {}), "drafts": ([3000, 70], [4, 2], 64, 8, {}),
+        "drafts, window": ([1000, 70], [6, 2], 32, 8, dict(window=3)), "chunk": ([900, 333], [500, 300], 32, 8, {}),
+        "chunk, window": ([900, 333], [500, 300], 32, 8, dict(window=100, sinks=3))}
+
+
+def some(shape, seed):
+    lens, nq, hq, hkv, kw = SOME[shape]
+    q, cache, table, cu = make(lens, nq, hq, hkv, 32, seed=seed)
+    slot = lens[0] - nq[0] + nq[0] // 2
+    assert 0 < sees(lens, nq, slot, **kw).sum() < nq[0]
+    return lens, nq, q, cache, table, cu, kw, slot, sees(lens, nq, slot, **kw)
+
+
+def check_unseen(got, want, mask, what):
+    """The rows that do not see the slot, against the statement without it."""
+    got = torch.where(mask[:, None, None].cuda(), want[0].to(got.dtype).cuda(), got)
+    ref.check_attention(got, want, what)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("bad", [dict(k_scale=math.nan), dict(k_scale=math.inf), dict(k_scale=-math.inf),
+                                 dict(k_zero=math.nan), dict(k_zero=-math.inf), dict(k_scale=math.inf, k_zero=0)])
+@pytest.mark.parametrize("shape", SOME)
+def test_key_scales_that_are_not_finite(spin_gpu, shape, bad, dtype):
+    """The rows that see the slot are NaN, the others do not know of it, in the same tile too."""
+    lens, nq, q, cache, table, cu, kw, slot, mask = some(shape, 2)
+    want = ref.attention(q, cache, table, lens, cu, **kw)
+    poison(cache, table, 32, slot, **bad)
+    got = run(spin_gpu, q, cache, table, lens, cu, out_dtype=dtype, **kw)
+    assert torch.isnan(got[mask]).all()
+    check_unseen(got, want, mask, "bf16" if dtype == BF16 else "")
+
+
+@pytest.mark.parametrize("scale", [60000.0, -60000.0, 2.0 ** -24, 0.0])
+@pytest.mark.parametrize("shape", SOME)
+def test_key_scales_far_apart(spin_gpu, shape, scale):
+    """One slot's key scale is far from the others': the rows that do not see it are as exact as ever,
+    and so are those that do."""
+    lens, nq, q, cache, table, cu, kw, slot, mask = some(shape, 3)
+    cache["k_scale"] *= 0.02
+    poison(cache, table, 32, slot, k_scale=scale)
+    kw = dict(kw, scale=2.5)
+    want = ref.attention(q, cache, table, lens, cu, **kw)
+    alone = dict(cache, k_scale=cache["k_scale"].clone())
+    poison(alone, table, 32, slot, k_scale=0.0)
+    s = ref.attention(q, alone, table, lens, cu, **kw)[2]  # size of the scores the unseeing rows meet
+    kw["softmax_scale"] = kw.pop("scale")
+    got = run(spin_gpu, q, cache, table, lens, cu, out_dtype=BF16, **kw)
+    check_unseen(got, (want[0], want[1], s, *want[3:]), mask, "bf16")
+    ref.check_attention(got, want, "bf16")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("most", [20, 57])
+@pytest.mark.parametrize("shape", ["drafts", "chunk", "chunk, window"])
+def test_large_scores(spin_gpu, shape, most, dtype):
+    """Queries that follow keys, whose elements are of one size: an error in a key's factor would be one
+    in every product of its score."""
+    lens, nq, q, cache, table, cu, kw, _, _ = some(shape, 4)
+    g = torch.Generator().manual_seed(5)
+    signs = torch.randint(0, 2, (64,), generator=g) * 12 + (torch.randint(0, 2, (64,), generator=g) * 12 << 4)
+    cache["k_cache"][:] = signs.to(torch.uint8).cuda()  # codes 0 and 12 about a zero of 6
+    cache["k_zero"].fill_(6)
+    cache["k_scale"] = (0.2 + 0.002 * torch.rand(cache["k_scale"].shape, generator=g)).half().cuda()
+    q[:] = torch.stack([signs & 15, signs >> 4], -1).flatten().cuda() / 6 - 1
+    scale = most / (6 * 0.201 * 128)
+    want = ref.attention(q, cache, table, lens, cu, scale=scale, **kw)
+    got = run(spin_gpu, q, cache, table, lens, cu, out_dtype=dtype, softmax_scale=scale, **kw)
+    ref.check_attention(got, want, "bf16" if dtype == BF16 else "")
+
+
+@pytest.mark.parametrize("shape", ["drafts", "chunk"])
+def test_query_rows_of_all_sizes(spin_gpu, shape):
+    """Rows of one tile from 2^-60 to 2^40 with a softmax scale for each, rows of zeros, and keys whose
+    scales keep the largest scores near 10."""
+    lens, nq, q, cache, table, cu, kw, _, _ = some(shape, 6)
+    g = torch.Generator().manual_seed(7)
+    for top in (0, 40):
+        e = torch.randint(-60, 1, q.shape[:2], generator=g).float() + top
+        e[::3] = top
+        rows = (torch.randn(q.shape, generator=g) * torch.exp2(e)[..., None]).bfloat16()
+        rows[1] = 0
+        rows = rows.cuda()
+        want = ref.attention(rows, cache, table, lens, cu, scale=2.0 ** -top / 10, **kw)
+        got = run(spin_gpu, rows, cache, table, lens, cu, out_dtype=BF16, softmax_scale=2.0 ** -top / 10, **kw)
+        ref.check_attention(got, want, "bf16")
