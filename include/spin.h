@@ -412,8 +412,8 @@ typedef struct spin_kv_pages_t {
  *   khat_j = (code_j - zero_j) * scale_j      (K and V alike, fp16 scale and zero)
  *   out_h = sum_j softmax_j(softmax_scale * (q_h . khat_j)) * vhat_j   over the visible slots
  * A token that sees no slot (a position below 0, lens[b] <= 0) gives 0. A NaN in a query row makes
- * that row of the result NaN; a slot whose key scale or zero is not finite does so to the rows that
- * see it. Sums are fp32. A weight is one fp16 number for bf16 results, two for fp32 ones; products
+ * that row of the result NaN; a slot with a scale or zero that is not finite does so to the rows
+ * that see it, and to no others. Sums are fp32. A weight is one fp16 number for bf16 results, two for fp32 ones; products
  * are exact, but in chunks of a prompt with bf16 results (more than 64 (token, query head) rows per
  * kv head) code - zero is rounded to fp16 where the zero is no whole number. The same call gives the
  * same bits.

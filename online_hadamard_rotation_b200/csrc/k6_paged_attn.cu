@@ -211,6 +211,7 @@ struct HalfVec {
     }
   }
   __device__ __forceinline__ uint32_t word(int i) const { return v[i]; }
+  __device__ __forceinline__ void clear(int i) { v[i >> 1] &= (i & 1) ? 0x0000FFFFu : 0xFFFF0000u; }
   __device__ __forceinline__ float at(int i) const {
     return __half2float(__ushort_as_half((unsigned short)((i & 1) ? v[i >> 1] >> 16 : v[i >> 1] & 0xFFFFu)));
   }
@@ -502,7 +503,6 @@ struct Worker {
           }
       }
       const bool odd = __any_sync(0xFFFFFFFFu, rest != 0u);
-      uint32_t dead = 0u;  // slots that no row sees
       const bool all_seen =
           j0 + BS - 1 <= first_pos && (a.window == 0 || j0 > last_pos - a.window || j0 + BS <= a.sinks);
       if (__any_sync(0xFFFFFFFFu, !all_seen || lost)) {
@@ -514,7 +514,7 @@ struct Worker {
               !lost && j <= last_pos && (a.window == 0 || j > first_pos - a.window || j < a.sinks);
           if (!some) {
             vsf[e] = 0.0f;
-            dead |= 1u << e;
+            hvz.clear(e);
           }
 #pragma unroll
           for (int n = 0; n < NT; ++n)
@@ -530,10 +530,31 @@ struct Worker {
 
       // ---- raise the rows' references where a weight could exceed them by too much: the
       // largest value scale of the block, as a power of two above it, counts with the scores
-      float vtop = 0.0f;
+      uint32_t vtop = 0u;
 #pragma unroll
-      for (int e = 0; e < S; ++e) vtop = fmaxf(vtop, fabsf(vsf[e]));
-      const uint32_t vbits = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(vtop));
+      for (int e = 0; e < S; ++e) vtop = max(vtop, __float_as_uint(fabsf(vsf[e])));
+      uint32_t vbits = __reduce_max_sync(0xFFFFFFFFu, vtop);
+      if (odd || vbits >= 0x7F800000u) {
+        // a value whose scale or zero is not finite makes NaN of the rows that see it by their scores,
+        // and is taken out of the products, where a weight of 0 would make NaN of the others too
+        vtop = 0u;
+#pragma unroll
+        for (int e = 0; e < S; ++e) {
+          if (!isfinite(vsf[e]) || !isfinite(hvz.at(e))) {
+            vsf[e] = 0.0f;
+            hvz.clear(e);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                float &x = sc[n][e >> 1][2 * (e & 1) + r];
+                x = x == -INFINITY ? x : NAN;
+              }
+          }
+          vtop = max(vtop, __float_as_uint(fabsf(vsf[e])));
+        }
+        vbits = __reduce_max_sync(0xFFFFFFFFu, vtop);
+      }
       const float vexp = (float)max((int)(vbits >> 23) - 126, -24);  // 2^-24: fp16's smallest
       bool over = false;
       float top[NT][2];
@@ -595,7 +616,7 @@ struct Worker {
         if (odd) {
 #pragma unroll
           for (int e = 0; e < S; ++e) {
-            const float vadd = (dead >> e & 1u) ? 0.0f : vsf[e] * zero_rest(hvz.word(e >> 1), e & 1);
+            const float vadd = vsf[e] * zero_rest(hvz.word(e >> 1), e & 1);
             z[n][0] = fmaf(ex2(fmaf(sc[n][e >> 1][2 * (e & 1)], qm[n][0], -m0)), vadd, z[n][0]);
             z[n][1] = fmaf(ex2(fmaf(sc[n][e >> 1][2 * (e & 1) + 1], qm[n][1], -m1)), vadd, z[n][1]);
           }

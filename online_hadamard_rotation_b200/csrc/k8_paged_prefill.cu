@@ -525,12 +525,14 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
       const int st = i & 1;
       const uint32_t ph = (uint32_t)(i >> 1) & 1u;
       // The scale a score meets is finite and above 0, so that it leaves the -inf of a hidden slot what
-      // it is: its sign is the key's, a scale of 0 becomes 2^-120, and where scale or zero is not
-      // finite the key is NaN.
+      // it is: its sign is the key's, and a scale of 0 becomes 2^-120. Where a scale or zero of the slot
+      // is not finite, its key is NaN (so are the rows that see it) and its value 0, since a weight of
+      // 0 would still make NaN of such a value in the rows that do not see it.
       const float kraw = __half2float(x.ks), kzero = __half2float(x.kz);
-      const bool sound = isfinite(kraw) && isfinite(kzero);
+      const float vraw = __half2float(x.vs), vzero = __half2float(x.vz);
+      const bool sound = isfinite(kraw) && isfinite(kzero) && isfinite(vraw) && isfinite(vzero);
       const float ks = x.has && sound ? fabsf(kraw) : 1.0f;
-      const float vs = x.has ? __half2float(x.vs) : 0.0f;
+      const float vs = x.has && sound ? vraw : 0.0f;
       // over the tile's slots: the exponent above the largest value scale, the ends of the key scales
       const uint32_t vb = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(vs)));
       const uint32_t kn = __reduce_min_sync(0xFFFFFFFFu, x.has ? __float_as_uint(ks) : 0x7F800000u);
@@ -566,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
         kmul = S.kmul;
       }
       {
-        const uint32_t z = twice(x.has ? __float2half_rn(__half2float(x.vz) * (-1.0f / 512.0f)) : zero);
+        const uint32_t z = twice(x.has && sound ? __float2half_rn(vzero * (-1.0f / 512.0f)) : zero);
         uint8_t *dst = smem + kOffV + st * kOperand;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {

@@ -152,3 +152,31 @@ def test_query_rows_of_all_sizes(spin_gpu, shape):
         want = ref.attention(rows, cache, table, lens, cu, scale=2.0 ** -top / 10, **kw)
         got = run(spin_gpu, rows, cache, table, lens, cu, out_dtype=BF16, softmax_scale=2.0 ** -top / 10, **kw)
         ref.check_attention(got, want, "bf16")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("bad", [dict(v_scale=math.nan), dict(v_scale=math.inf), dict(v_scale=-math.inf),
+                                 dict(v_zero=math.nan), dict(v_zero=math.inf), dict(v_zero=-math.inf, v_scale=0)])
+@pytest.mark.parametrize("shape", SOME)
+def test_value_scales_that_are_not_finite(spin_gpu, shape, bad, dtype):
+    """As for keys: a weight of 0 leaves nothing of such a value in the rows that do not see it."""
+    lens, nq, q, cache, table, cu, kw, slot, mask = some(shape, 8)
+    want = ref.attention(q, cache, table, lens, cu, **kw)
+    poison(cache, table, 32, slot, **bad)
+    got = run(spin_gpu, q, cache, table, lens, cu, out_dtype=dtype, **kw)
+    assert torch.isnan(got[mask]).all()
+    check_unseen(got, want, mask, "bf16" if dtype == BF16 else "")
+
+
+def test_value_scales_that_are_not_finite_among_zeros_between_the_codes(spin_gpu):
+    from tests.test_gpu_paged_attn import odd_zeros
+    for shape in SOME:
+        lens, nq, q, cache, table, cu, kw, slot, mask = some(shape, 9)
+        want = odd_zeros(q, cache, table, lens, cu, 10, **kw)
+        poison(cache, table, 32, slot, v_zero=math.nan)
+        poison(cache, table, 32, slot + 1, v_scale=math.inf)
+        for dtype in (F32, BF16):
+            got = run(spin_gpu, q, cache, table, lens, cu, out_dtype=dtype, **kw)
+            seen = mask | sees(lens, nq, slot + 1, **kw)
+            assert torch.isnan(got[seen]).all()
+            check_unseen(got, want, seen, "prefill" if dtype == BF16 else "")
