@@ -48,8 +48,8 @@
 // each on the copy engine and were slower. (Loads straight into registers, 32 slots a block at the
 // same occupancy: 83 us against 67 on 4 rows of up to 65537 slots, fp32.)
 // The softmax keeps one reference per row that is raised only when a weight could pass 2^14 (a
-// raised one leaves 2^9), so most blocks need no cross-lane maximum; fp16's smallest step is then
-// 2^-33 of the row's largest weight or less.
+// raised one leaves 2^8 .. 2^9), so most blocks need no cross-lane maximum; the largest w of a row is
+// then 2^8 or more, and half of fp16's smallest step is 2^-33 of it or less.
 //
 // Work is divided over a fixed number of warps: the list of all (sequence, kv head, row tile)
 // items, each as many units long as its sequence has slot blocks and cuts.item more for its fixed
@@ -528,8 +528,9 @@ struct Worker {
         }
       }
 
-      // ---- raise the rows' references where a weight could exceed them by too much: the
-      // largest value scale of the block, as a power of two above it, counts with the scores
+      // ---- raise the rows' references where a weight could exceed them by too much: a slot's value
+      // scale, as a power of two above it, counts with its score. The largest of each bound them all;
+      // the slots' own sums are looked at where that is not enough.
       uint32_t vtop = 0u;
 #pragma unroll
       for (int e = 0; e < S; ++e) vtop = max(vtop, __float_as_uint(fabsf(vsf[e])));
@@ -555,9 +556,8 @@ struct Worker {
         }
         vbits = __reduce_max_sync(0xFFFFFFFFu, vtop);
       }
-      const float vexp = (float)max((int)(vbits >> 23) - 126, -24);  // 2^-24: fp16's smallest
+      const float vexp = scale_exponent(__uint_as_float(vbits));
       bool over = false;
-      float top[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -565,15 +565,19 @@ struct Worker {
           float v = sc[n][0][r];
 #pragma unroll
           for (int e = 1; e < S; ++e) v = fmaxf(v, sc[n][e >> 1][2 * (e & 1) + r]);
-          top[n][r] = fmaf(v, qm[n][r], vexp);
-          over |= top[n][r] > m[n][r] + kRaise + kRoom;  // false while both are -inf
+          over |= fmaf(v, qm[n][r], vexp) > m[n][r] + kRaise + kRoom;  // false while both are -inf
         }
       if (__any_sync(0xFFFFFFFFu, over)) {
+        float ve[S];
+#pragma unroll
+        for (int e = 0; e < S; ++e) ve[e] = scale_exponent(vsf[e]);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            float v = top[n][r];
+            float v = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < S; ++e) v = fmaxf(v, fmaf(sc[n][e >> 1][2 * (e & 1) + r], qm[n][r], ve[e]));
             v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
             v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));

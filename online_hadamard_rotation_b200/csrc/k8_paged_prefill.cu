@@ -12,7 +12,7 @@
 //   scores, the values' the weights, so no key scale reaches another slot or a row that does not see
 //   it. (In the keys' operand they cost a rounding of each key, whose errors add up where a query
 //   follows a key, and what the scales have in common; the call measured below took 312 us so, and
-//   339 with the scores' 128 shared-memory reads and the look at the bound.)
+//   341 with the scores' 128 shared-memory reads and the look at the bound.)
 // as K-major and MN-major operands with the 128-byte swizzle (eight codes of a word come out in
 // the order 0, 4, 1, 5, 2, 6, 3, 7; the queries are packed alike and the output is put back).
 // Queries are scaled by a power of two, one for the block where its rows allow it (the keys' scales
@@ -59,8 +59,13 @@ constexpr int kRows = 256;      // rows of a block of threads, two halves of 128
 constexpr int kTile = 128;      // slots of a tile
 constexpr uint32_t kOperand = kTile * kD * 2;  // bytes of a 128 x 128 fp16 operand
 constexpr uint32_t kOffQ = 0, kOffK = 2 * kOperand, kOffV = 4 * kOperand, kOffS = 6 * kOperand;
-constexpr float kRoom = 9.0f;   // a raised reference leaves weights at most 2^kRoom
-constexpr float kRaise = 5.0f;  // log2 above that at which it is raised again (fp16 ends at 2^16)
+// A raised reference leaves weights at most 2^kRoom, and is raised again where one could exceed that by
+// 2^kRaise (fp16 ends at 2^16). The largest weight of a row is 2^(kRoom - 1) or more then, and half of
+// fp16's smallest step 2^-28 of it, enough for bf16 results. The bound's slack is what kRaise leaves
+// over: with 9 and 5 the call measured above looks at the slots in most tiles and takes 422 us, with 6
+// and 8 or 3 and 12 as long as so.
+constexpr float kRoom = 4.0f;
+constexpr float kRaise = 10.0f;
 constexpr float kCode = 512.0f; // what the codes' 2^-9 takes out
 constexpr long long kTimeoutCycles = 4000000000LL;  // about two seconds
 
@@ -182,16 +187,10 @@ __device__ __forceinline__ int load_ahead(const int32_t *p) {
   return v;
 }
 
-// 64 scores times their slots' key scales.
-__device__ __forceinline__ void scale_keys(uint32_t (&x)[64], const float *ks) {
+// 64 scores times their slots' key scales, plus the exponents above their value scales.
+__device__ __forceinline__ void scale_scores(uint32_t (&x)[64], const float *ks, const float *vs) {
 #pragma unroll
-  for (int k = 0; k < 64; k += 4) {
-    const float4 s = *reinterpret_cast<const float4 *>(ks + k);
-    const float2 a = mul2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), make_float2(s.x, s.y));
-    const float2 b = mul2(make_float2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])), make_float2(s.z, s.w));
-    x[k] = __float_as_uint(a.x), x[k + 1] = __float_as_uint(a.y);
-    x[k + 2] = __float_as_uint(b.x), x[k + 3] = __float_as_uint(b.y);
-  }
+  for (int k = 0; k < 64; ++k) x[k] = __float_as_uint(fmaf(__uint_as_float(x[k]), ks[k], scale_exponent(vs[k])));
 }
 
 __device__ __forceinline__ float largest(const uint32_t (&x)[64]) {  // NaN among them do not count
@@ -381,11 +380,12 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
         }
         tmem_wait_st();
       }
-      // ---- can a weight exceed the row's reference by too much? The largest raw score times the ends
-      // of the tile's key scales bounds the scores; where that is not enough (the first tile, large
-      // scores), the scores are read once more and scaled one by one. (Every row reads its scores
-      // twice or more: 128 registers for them would spill, and what spills is read back through an L1
-      // that shared memory leaves small.)
+      // ---- can a weight exceed the row's reference by too much? A slot's value scale, as a power of two
+      // above it, counts with its score. The largest raw score times the ends of the tile's key scales
+      // and the largest value scale bound them all; where that is not enough (the first tile, large
+      // scores, scales far apart), the scores are read once more and scaled slot by slot. (Every row
+      // reads its scores twice or more: 128 registers for them would spill, and what spills is read
+      // back through an L1 that shared memory leaves small.)
       float top = -INFINITY;
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
@@ -405,10 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
           tc::tmem_ld32(s_at + 64u * c, x);
           tc::tmem_ld32(s_at + 64u * c + 32u, x + 32);
           tc::tmem_wait_ld();
-          scale_keys(x, &S.ks[st][64 * c]);
+          scale_scores(x, &S.ks[st][64 * c], &S.vs[st][64 * c]);
           top = fmaxf(top, largest(x));
         }
-        top += vexp;
       }
       // ---- raise the reference where a weight could exceed it by too much
       const bool raise = top > m + kRoom + kRaise;  // false while both are -inf
@@ -580,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
         S.vs[st][c] = vs;
         if (lane == 0) S.seen[st][cw] = has;
         if (c == 0) {
-          S.vexp[st] = (float)max((int)(over(most, S.wvmax[st]) >> 23) - 126, -24);
+          S.vexp[st] = scale_exponent(__uint_as_float(over(most, S.wvmax[st])));
           S.kmin[st] = fmaxf(__uint_as_float(over(least, S.wkmin[st])) * kmul, 0x1p-120f);
           S.kmax[st] = fmaxf(__uint_as_float(over(most, S.wkmax[st])) * kmul, 0x1p-120f);
         }

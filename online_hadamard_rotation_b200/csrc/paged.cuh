@@ -57,6 +57,11 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// The exponent above a value scale, at least that of fp16's smallest number: 2^(e - 1) <= |s| < 2^e.
+__device__ __forceinline__ float scale_exponent(float s) {
+  return (float)max((int)((__float_as_uint(s) >> 23) & 255u) - 126, -24);
+}
+
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));

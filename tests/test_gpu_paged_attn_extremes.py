@@ -180,3 +180,51 @@ def test_value_scales_that_are_not_finite_among_zeros_between_the_codes(spin_gpu
             seen = mask | sees(lens, nq, slot + 1, **kw)
             assert torch.isnan(got[seen]).all()
             check_unseen(got, want, seen, "prefill" if dtype == BF16 else "")
+
+
+def weight_floor(q, cache, table, lens, cu, page, scale, window=0, sinks=0):
+    """Per element max_j p_j |s_j| times sum_j |c_j - z_j|: a weight p_j s_j ends at steps of 2^-24 where a
+    row's largest is 2^8 or more, so half a step is 2^-33 of that for each slot; 2^3 and 2^-28 in the
+    kernel for chunks."""
+    tokens, hq, _ = q.shape
+    hkv, out = cache["k_cache"].shape[1], torch.zeros(q.shape, dtype=torch.float64)
+    for b, n in enumerate(lens):
+        slots = torch.arange(n)
+        ids = table[b].cpu()[slots // page].long()
+
+        def rows(name):
+            x = cache[name + "_cache"].cpu()[ids, :, slots % page]
+            z, s = (cache[name + e].cpu()[ids, :, slots % page].double()[..., None] for e in ("_zero", "_scale"))
+            return torch.stack([x & 15, x >> 4], -1).flatten(-2).double() - z, s  # [n, hkv, 128]
+
+        (k, ks), (v, vs) = rows("k"), rows("v")
+        p = torch.arange(n - (cu[b + 1] - cu[b]), n)[:, None]
+        hidden = (slots > p) | ((p - slots >= window) & (slots >= sinks) if window else torch.zeros(()).bool())
+        for h in range(hq):
+            g = h * hkv // hq
+            score = q[cu[b]:cu[b + 1], h].double().cpu() @ (k * ks)[:, g].T * scale
+            w = torch.softmax(score.masked_fill(hidden, -math.inf), 1) * vs[:, g, 0].abs()
+            out[cu[b]:cu[b + 1], h] = w.amax(1, keepdim=True) * ((~hidden).double() @ v[:, g].abs())
+    return out
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("small", [2.0 ** -16, 2.0 ** -9])
+@pytest.mark.parametrize("shape", SOME)
+def test_value_scales_far_apart(spin_gpu, shape, small, dtype):
+    """One slot has a value scale of 60000 and scores below the others' by about 25, the others have scales
+    of 2^-16 or 2^-9: neither its scale nor its tile's largest one may cost the others their bits, in the
+    rows that see it and in those that do not."""
+    lens, nq, q, cache, table, cu, kw, slot, mask = some(shape, 11)
+    g = torch.Generator().manual_seed(12)
+    q += 1
+    cache["v_scale"] = (small * (1 + torch.rand(cache["v_scale"].shape, generator=g))).half().cuda()
+    cache["k_scale"] *= 0.1
+    poison(cache, table, 32, slot, v_scale=60000.0, k_scale=0.28, k_zero=8)
+    cache["k_cache"][table[0, slot // 32].item(), :, slot % 32] = 0
+    want = ref.attention(q, cache, table, lens, cu, **kw)
+    floor = weight_floor(q, cache, table, lens, cu, 32, 128 ** -0.5, **kw)
+    if dtype == BF16 and shape.startswith("chunk"):
+        floor = 32 * floor
+    got = run(spin_gpu, q, cache, table, lens, cu, out_dtype=dtype, **kw)
+    ref.check_attention(got, (*want[:3], floor, want[4]), "bf16" if dtype == BF16 else "")
