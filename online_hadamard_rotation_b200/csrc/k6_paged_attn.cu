@@ -108,6 +108,11 @@ constexpr int kWholeUnits = 16;
 // 68.8 and 62.9.
 constexpr int kNarrowRows = 64;
 constexpr int kPart = 132;     // floats per row of a piece: 128 sums, max, sum of weights, pad
+// The tensor cores truncate as they add, so a long chain of products is too small: 1.2e-3 of the result
+// over 262144 slots, 6.9e-3 over 2^20. A chain of value products ends after this many, 2^-23 of it each
+// at most, 2^-15 together. (The loop around the chains costs 3 % where none is long: 32 sequences of up
+// to 4096 slots 30.9 us a call without, 31.9 with; a test in the blocks' loop 32.5.)
+constexpr int kChain = 256;
 constexpr float kRoom = 9.0f;   // a raised reference leaves weights at most 2^kRoom
 constexpr float kRaise = 5.0f;  // log2 above that at which it is raised again (fp16 ends at 2^16)
 
@@ -381,6 +386,25 @@ struct Worker {
 
     float(&acc)[NT][8][4] = chain_of(o, own);  // where the value products add up
     int chain = 0;
+    // bf16 results: the sums of the chains that ended, of their weights, and the reference they have.
+    // Touched too rarely for registers.
+    volatile float ended[F32 ? 1 : NT * 2][18];
+    bool more = false;
+    auto add_ended = [&]() {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          volatile float *was = ended[2 * n + r];
+          const float f = m[n][r] == -INFINITY ? 1.0f : ex2(was[17] - m[n][r]);
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            o[n][t][r] = fmaf(was[2 * t], f, o[n][t][r]);
+            o[n][t][2 + r] = fmaf(was[2 * t + 1], f, o[n][t][2 + r]);
+          }
+          l[n][r] = fmaf(was[16], f, l[n][r]);
+        }
+    };
 
     auto start_of = [&](int k) { return (k < bl.nsink ? k : k - bl.nsink + bl.first) * BS; };
     // this tile's part of the sequence's blocks: not behind its last row, nor before its first
@@ -428,254 +452,279 @@ struct Worker {
       fetch(0, page0, start_of(i));
       fetch(1, page0, start_of(i));
     }
-    for (; i < end; ++i) {
-      const int j0 = start_of(i);
-      // the group's slots lie in 16-slot part S g / 16 of the block: has it a page?
-      const bool lost = (__ballot_sync(0xFFFFFFFFu, page0 < 0) >> (S * g / 16)) & 1u;
-      const int page2 = i + 2 < end ? page_at(i + 2) : -1;
-      copy_wait<1>();
-      HalfVec<S> hks, hkz;
-      hks.load(&st.steps[0][S * g]);
-      hkz.load(&st.steps[1][S * g]);
+    while (i < end) {  // chains of products (one, for fp32 results, which add up as they go)
+      const int stop = F32 ? end : min(end, i + kChain / MT);
+#pragma unroll 1
+      for (; i < stop; ++i) {
+        const int j0 = start_of(i);
+        // the group's slots lie in 16-slot part S g / 16 of the block: has it a page?
+        const bool lost = (__ballot_sync(0xFFFFFFFFu, page0 < 0) >> (S * g / 16)) & 1u;
+        const int page2 = i + 2 < end ? page_at(i + 2) : -1;
+        copy_wait<1>();
+        HalfVec<S> hks, hkz;
+        hks.load(&st.steps[0][S * g]);
+        hkz.load(&st.steps[1][S * g]);
 #pragma unroll
-      for (int k = 0; k < S / 2; ++k) {  // what is not finite becomes NaN, and so the slot's scores
-        hks.v[k] = fma_f16x2(hks.v[k], 0u, hks.v[k]);
-        hkz.v[k] = fma_f16x2(hkz.v[k], 0u, hkz.v[k]);
-      }
+        for (int k = 0; k < S / 2; ++k) {  // what is not finite becomes NaN, and so the slot's scores
+          hks.v[k] = fma_f16x2(hks.v[k], 0u, hks.v[k]);
+          hkz.v[k] = fma_f16x2(hkz.v[k], 0u, hkz.v[k]);
+        }
 
-      // ---- scores: sc[n][t][..] = (slot of row g: rows 2c, 2c + 1; of row g + 8: the same)
-      float sc[NT][MT][4];
-      // all of a thread's key codes first, then k steps with one product per tile: MT sums are under
-      // way at a time
-      uint4 kx[MT], ky[MT];
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const uint8_t *key = st.keys + g * Stage<MT>::kKeyRun + 2 * t * 64 + 16 * c;
-        kx[t] = *reinterpret_cast<const uint4 *>(key);
-        ky[t] = *reinterpret_cast<const uint4 *>(key + 64);
-      }
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {  // k steps of 16 elements
-        uint2 qf[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) qf[n] = sm.qfrag[warp][n][u][lane];
+        // ---- scores: sc[n][t][..] = (slot of row g: rows 2c, 2c + 1; of row g + 8: the same)
+        float sc[NT][MT][4];
+        // all of a thread's key codes first, then k steps with one product per tile: MT sums are under
+        // way at a time
+        uint4 kx[MT], ky[MT];
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-          const uint32_t wx = (u >> 1) == 0 ? kx[t].x : (u >> 1) == 1 ? kx[t].y : (u >> 1) == 2 ? kx[t].z : kx[t].w;
-          const uint32_t wy = (u >> 1) == 0 ? ky[t].x : (u >> 1) == 1 ? ky[t].y : (u >> 1) == 2 ? ky[t].z : ky[t].w;
-          const uint32_t x = (u & 1) ? wx >> 8 : wx, v = (u & 1) ? wy >> 8 : wy;
-          const uint32_t a0 = x & 0x000F000Fu, a1 = v & 0x000F000Fu, a2 = x & 0x00F000F0u, a3 = v & 0x00F000F0u;
+          const uint8_t *key = st.keys + g * Stage<MT>::kKeyRun + 2 * t * 64 + 16 * c;
+          kx[t] = *reinterpret_cast<const uint4 *>(key);
+          ky[t] = *reinterpret_cast<const uint4 *>(key + 64);
+        }
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if (u == 0) mma_f16_first(sc[n][t], a0, a1, a2, a3, qf[n].x, qf[n].y);
-            else mma_f16(sc[n][t], a0, a1, a2, a3, qf[n].x, qf[n].y);
+        for (int u = 0; u < 8; ++u) {  // k steps of 16 elements
+          uint2 qf[NT];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) qf[n] = sm.qfrag[warp][n][u][lane];
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            const uint32_t wx = (u >> 1) == 0 ? kx[t].x : (u >> 1) == 1 ? kx[t].y : (u >> 1) == 2 ? kx[t].z : kx[t].w;
+            const uint32_t wy = (u >> 1) == 0 ? ky[t].x : (u >> 1) == 1 ? ky[t].y : (u >> 1) == 2 ? ky[t].z : ky[t].w;
+            const uint32_t x = (u & 1) ? wx >> 8 : wx, v = (u & 1) ? wy >> 8 : wy;
+            const uint32_t a0 = x & 0x000F000Fu, a1 = v & 0x000F000Fu, a2 = x & 0x00F000F0u, a3 = v & 0x00F000F0u;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              if (u == 0) mma_f16_first(sc[n][t], a0, a1, a2, a3, qf[n].x, qf[n].y);
+              else mma_f16(sc[n][t], a0, a1, a2, a3, qf[n].x, qf[n].y);
+            }
           }
         }
-      }
 
-      // ---- the next block's keys may take this one's place
-      __syncwarp();
-      if (i + 1 < end) {
-        fetch(0, page1, start_of(i + 1));
-        copy_wait<1>();
-      } else {
-        copy_wait<0>();
-      }
-      HalfVec<S> hvs, hvz;
-      hvs.load(&st.steps[2][S * g]);
-      hvz.load(&st.steps[3][S * g]);
+        // ---- the next block's keys may take this one's place
+        __syncwarp();
+        if (i + 1 < end) {
+          fetch(0, page1, start_of(i + 1));
+          copy_wait<1>();
+        } else {
+          copy_wait<0>();
+        }
+        HalfVec<S> hvs, hvz;
+        hvs.load(&st.steps[2][S * g]);
+        hvz.load(&st.steps[3][S * g]);
 
-      // ---- scores with the slot's scale and zero (still without the row's factor)
-      float vsf[S];
-      uint32_t rest = 0u;  // nonzero where a value zero is not one of the whole numbers 0 .. 15
-#pragma unroll
-      for (int e = 0; e < S; ++e) {
-        const float kmul = hks.at(e) * kHalfKey;
-        const float kadd = kmul * hkz.at(e) * (-1.0f / (kHalfKey * kHalfKey));
-        vsf[e] = hvs.at(e);
-        if ((e & 1) == 0) rest |= zeros_rest(hvz.word(e >> 1));
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            float &x = sc[n][e >> 1][2 * (e & 1) + r];
-            x = fmaf(kadd, qs[n][r], kmul * x);
-          }
-      }
-      const bool odd = __any_sync(0xFFFFFFFFu, rest != 0u);
-      const bool all_seen =
-          j0 + BS - 1 <= first_pos && (a.window == 0 || j0 > last_pos - a.window || j0 + BS <= a.sinks);
-      if (__any_sync(0xFFFFFFFFu, !all_seen || lost)) {
+        // ---- scores with the slot's scale and zero (still without the row's factor)
+        float vsf[S];
+        uint32_t rest = 0u;  // nonzero where a value zero is not one of the whole numbers 0 .. 15
 #pragma unroll
         for (int e = 0; e < S; ++e) {
-          const int j = j0 + S * g + e;
-          // a slot no row sees may hold anything, NaN scales too: take it out of the sums
-          const bool some =
-              !lost && j <= last_pos && (a.window == 0 || j > first_pos - a.window || j < a.sinks);
-          if (!some) {
-            vsf[e] = 0.0f;
-            hvz.clear(e);
-          }
+          const float kmul = hks.at(e) * kHalfKey;
+          const float kadd = kmul * hkz.at(e) * (-1.0f / (kHalfKey * kHalfKey));
+          vsf[e] = hvs.at(e);
+          if ((e & 1) == 0) rest |= zeros_rest(hvz.word(e >> 1));
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              const int p = sm.pos[warp][8 * n + 2 * c + r];
-              const bool seen = some && j <= p && (a.window == 0 || j > p - a.window || j < a.sinks);
               float &x = sc[n][e >> 1][2 * (e & 1) + r];
-              x = seen ? x : -INFINITY;
+              x = fmaf(kadd, qs[n][r], kmul * x);
             }
         }
-      }
-
-      // ---- raise the rows' references where a weight could exceed them by too much: a slot's value
-      // scale, as a power of two above it, counts with its score. The largest of each bound them all;
-      // the slots' own sums are looked at where that is not enough.
-      uint32_t vtop = 0u;
+        const bool odd = __any_sync(0xFFFFFFFFu, rest != 0u);
+        const bool all_seen =
+            j0 + BS - 1 <= first_pos && (a.window == 0 || j0 > last_pos - a.window || j0 + BS <= a.sinks);
+        if (__any_sync(0xFFFFFFFFu, !all_seen || lost)) {
 #pragma unroll
-      for (int e = 0; e < S; ++e) vtop = max(vtop, __float_as_uint(fabsf(vsf[e])));
-      uint32_t vbits = __reduce_max_sync(0xFFFFFFFFu, vtop);
-      if (odd || vbits >= 0x7F800000u) {
-        // a value whose scale or zero is not finite makes NaN of the rows that see it by their scores,
-        // and is taken out of the products, where a weight of 0 would make NaN of the others too
-        vtop = 0u;
-#pragma unroll
-        for (int e = 0; e < S; ++e) {
-          if (!isfinite(vsf[e]) || !isfinite(hvz.at(e))) {
-            vsf[e] = 0.0f;
-            hvz.clear(e);
+          for (int e = 0; e < S; ++e) {
+            const int j = j0 + S * g + e;
+            // a slot no row sees may hold anything, NaN scales too: take it out of the sums
+            const bool some =
+                !lost && j <= last_pos && (a.window == 0 || j > first_pos - a.window || j < a.sinks);
+            if (!some) {
+              vsf[e] = 0.0f;
+              hvz.clear(e);
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
               for (int r = 0; r < 2; ++r) {
+                const int p = sm.pos[warp][8 * n + 2 * c + r];
+                const bool seen = some && j <= p && (a.window == 0 || j > p - a.window || j < a.sinks);
                 float &x = sc[n][e >> 1][2 * (e & 1) + r];
-                x = x == -INFINITY ? x : NAN;
+                x = seen ? x : -INFINITY;
               }
           }
-          vtop = max(vtop, __float_as_uint(fabsf(vsf[e])));
         }
-        vbits = __reduce_max_sync(0xFFFFFFFFu, vtop);
-      }
-      const float vexp = scale_exponent(__uint_as_float(vbits));
-      bool over = false;
+
+        // ---- raise the rows' references where a weight could exceed them by too much: a slot's value
+        // scale, as a power of two above it, counts with its score. The largest of each bound them all;
+        // the slots' own sums are looked at where that is not enough.
+        uint32_t vtop = 0u;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+        for (int e = 0; e < S; ++e) vtop = max(vtop, __float_as_uint(fabsf(vsf[e])));
+        uint32_t vbits = __reduce_max_sync(0xFFFFFFFFu, vtop);
+        if (odd || vbits >= 0x7F800000u) {
+          // a value whose scale or zero is not finite makes NaN of the rows that see it by their scores,
+          // and is taken out of the products, where a weight of 0 would make NaN of the others too
+          vtop = 0u;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float v = sc[n][0][r];
+          for (int e = 0; e < S; ++e) {
+            if (!isfinite(vsf[e]) || !isfinite(hvz.at(e))) {
+              vsf[e] = 0.0f;
+              hvz.clear(e);
 #pragma unroll
-          for (int e = 1; e < S; ++e) v = fmaxf(v, sc[n][e >> 1][2 * (e & 1) + r]);
-          over |= fmaf(v, qm[n][r], vexp) > m[n][r] + kRaise + kRoom;  // false while both are -inf
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                  float &x = sc[n][e >> 1][2 * (e & 1) + r];
+                  x = x == -INFINITY ? x : NAN;
+                }
+            }
+            vtop = max(vtop, __float_as_uint(fabsf(vsf[e])));
+          }
+          vbits = __reduce_max_sync(0xFFFFFFFFu, vtop);
         }
-      if (__any_sync(0xFFFFFFFFu, over)) {
-        float ve[S];
-#pragma unroll
-        for (int e = 0; e < S; ++e) ve[e] = scale_exponent(vsf[e]);
+        const float vexp = scale_exponent(__uint_as_float(vbits));
+        bool over = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            float v = -INFINITY;
+            float v = sc[n][0][r];
 #pragma unroll
-            for (int e = 0; e < S; ++e) v = fmaxf(v, fmaf(sc[n][e >> 1][2 * (e & 1) + r], qm[n][r], ve[e]));
-            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
-            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
-            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
-            const float mn = fmaxf(m[n][r], v - kRoom);
-            const float f = mn == -INFINITY ? 1.0f : ex2(m[n][r] - mn);
-            m[n][r] = mn;
-            l[n][r] *= f;
-            z[n][r] *= f;
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-              o[n][t][r] *= f;
-              o[n][t][2 + r] *= f;
-              if constexpr (F32) {
-                acc[n][t][r] *= f;
-                acc[n][t][2 + r] *= f;
-              }
-            }
+            for (int e = 1; e < S; ++e) v = fmaxf(v, sc[n][e >> 1][2 * (e & 1) + r]);
+            over |= fmaf(v, qm[n][r], vexp) > m[n][r] + kRaise + kRoom;  // false while both are -inf
           }
-      }
-
-      // ---- weights in B layout (slots along k): one fp16 term, for fp32 results two
-      uint32_t ph[NT][S], pl[F32 ? NT : 1][S];
+        if (__any_sync(0xFFFFFFFFu, over)) {
+          float ve[S];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float m0 = m[n][0] == -INFINITY ? 0.0f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.0f : m[n][1];
-#pragma unroll
-        for (int e = 0; e < S; ++e) {
-          const float p0 = ex2(fmaf(sc[n][e >> 1][2 * (e & 1)], qm[n][0], -m0));
-          const float p1 = ex2(fmaf(sc[n][e >> 1][2 * (e & 1) + 1], qm[n][1], -m1));
-          const float w0 = p0 * vsf[e], w1 = p1 * vsf[e];
-          l[n][0] += p0;
-          l[n][1] += p1;
-          const uint32_t hi = pack_f16x2(w0, w1);
-          ph[n][e] = movmatrix(hi);
-          if constexpr (F32) {
-            const float2 hf = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-            pl[n][e] = movmatrix(pack_f16x2(w0 - hf.x, w1 - hf.y));
-          }
-        }
-        if (odd) {
-#pragma unroll
-          for (int e = 0; e < S; ++e) {
-            const float vadd = vsf[e] * zero_rest(hvz.word(e >> 1), e & 1);
-            z[n][0] = fmaf(ex2(fmaf(sc[n][e >> 1][2 * (e & 1)], qm[n][0], -m0)), vadd, z[n][0]);
-            z[n][1] = fmaf(ex2(fmaf(sc[n][e >> 1][2 * (e & 1) + 1], qm[n][1], -m1)), vadd, z[n][1]);
-          }
-        }
-      }
-
-      // ---- values
-      HalfVec<S> vz0, vz1;  // zeros of the thread's slots
-      vz0.load(&st.steps[3][2 * S * c]);
-      vz1.load(&st.steps[3][2 * S * c + S]);
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        // slots 2t and 2t + 1 of the thread's two runs
-        const uint8_t *v0 = st.values + 2 * c * Stage<MT>::kValueRun + 2 * t * 64 + 8 * g;
-        const uint8_t *v1 = v0 + Stage<MT>::kValueRun;
-        const uint2 s0 = *reinterpret_cast<const uint2 *>(v0), s1 = *reinterpret_cast<const uint2 *>(v1);
-        const uint2 s2 = *reinterpret_cast<const uint2 *>(v0 + 64), s3 = *reinterpret_cast<const uint2 *>(v1 + 64);
-        const uint32_t zx = zeros_f16(__byte_perm(vz0.word(t), vz1.word(t), 0x5410)),
-                       zy = zeros_f16(__byte_perm(vz0.word(t), vz1.word(t), 0x7632));
-#pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) {  // four elements: 16 g + 4 q4 .. + 3
-          const uint32_t w0 = q4 < 2 ? s0.x : s0.y, w1 = q4 < 2 ? s1.x : s1.y, w2 = q4 < 2 ? s2.x : s2.y,
-                         w3 = q4 < 2 ? s3.x : s3.y;
-          const uint32_t sel = (q4 & 1) ? 0x7632u : 0x5410u;
-          uint32_t x = __byte_perm(w0, w1, sel), y = __byte_perm(w2, w3, sel);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t a0 = codes_lo(x, zx), a1 = codes_hi(x, zx), a2 = codes_lo(y, zy), a3 = codes_hi(y, zy);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma_f16(acc[n][2 * q4 + k], a0, a1, a2, a3, ph[n][2 * t], ph[n][2 * t + 1]);
-              if constexpr (F32) mma_f16(acc[n][2 * q4 + k], a0, a1, a2, a3, pl[n][2 * t], pl[n][2 * t + 1]);
-            }
-            x >>= 8;
-            y >>= 8;
-          }
-        }
-      }
-      __syncwarp();
-      if (i + 1 < end) fetch(1, page1, start_of(i + 1));
-      page0 = page1;
-      page1 = page2;
-      if constexpr (F32) {
-        // the tensor cores truncate each sum, so a long chain is a little too small (1.4e-6 of the
-        // norm over 870 slots): fp32 results take the chain to a rounded sum every few blocks
-        if ((++chain & 3) == 0 || i + 1 == end) {
+          for (int e = 0; e < S; ++e) ve[e] = scale_exponent(vsf[e]);
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int t = 0; t < 8; ++t)
+            for (int r = 0; r < 2; ++r) {
+              float v = -INFINITY;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                o[n][t][e] += acc[n][t][e];
-                acc[n][t][e] = 0.0f;
+              for (int e = 0; e < S; ++e) v = fmaxf(v, fmaf(sc[n][e >> 1][2 * (e & 1) + r], qm[n][r], ve[e]));
+              v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
+              v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
+              v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+              const float mn = fmaxf(m[n][r], v - kRoom);
+              const float f = mn == -INFINITY ? 1.0f : ex2(m[n][r] - mn);
+              m[n][r] = mn;
+              l[n][r] *= f;
+              z[n][r] *= f;
+#pragma unroll
+              for (int t = 0; t < 8; ++t) {
+                o[n][t][r] *= f;
+                o[n][t][2 + r] *= f;
+                if constexpr (F32) {
+                  acc[n][t][r] *= f;
+                  acc[n][t][2 + r] *= f;
+                }
               }
+            }
+        }
+
+        // ---- weights in B layout (slots along k): one fp16 term, for fp32 results two
+        uint32_t ph[NT][S], pl[F32 ? NT : 1][S];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float m0 = m[n][0] == -INFINITY ? 0.0f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.0f : m[n][1];
+#pragma unroll
+          for (int e = 0; e < S; ++e) {
+            const float p0 = ex2(fmaf(sc[n][e >> 1][2 * (e & 1)], qm[n][0], -m0));
+            const float p1 = ex2(fmaf(sc[n][e >> 1][2 * (e & 1) + 1], qm[n][1], -m1));
+            const float w0 = p0 * vsf[e], w1 = p1 * vsf[e];
+            l[n][0] += p0;
+            l[n][1] += p1;
+            const uint32_t hi = pack_f16x2(w0, w1);
+            ph[n][e] = movmatrix(hi);
+            if constexpr (F32) {
+              const float2 hf = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+              pl[n][e] = movmatrix(pack_f16x2(w0 - hf.x, w1 - hf.y));
+            }
+          }
+          if (odd) {
+#pragma unroll
+            for (int e = 0; e < S; ++e) {
+              const float vadd = vsf[e] * zero_rest(hvz.word(e >> 1), e & 1);
+              z[n][0] = fmaf(ex2(fmaf(sc[n][e >> 1][2 * (e & 1)], qm[n][0], -m0)), vadd, z[n][0]);
+              z[n][1] = fmaf(ex2(fmaf(sc[n][e >> 1][2 * (e & 1) + 1], qm[n][1], -m1)), vadd, z[n][1]);
+            }
+          }
+        }
+
+        // ---- values
+        HalfVec<S> vz0, vz1;  // zeros of the thread's slots
+        vz0.load(&st.steps[3][2 * S * c]);
+        vz1.load(&st.steps[3][2 * S * c + S]);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          // slots 2t and 2t + 1 of the thread's two runs
+          const uint8_t *v0 = st.values + 2 * c * Stage<MT>::kValueRun + 2 * t * 64 + 8 * g;
+          const uint8_t *v1 = v0 + Stage<MT>::kValueRun;
+          const uint2 s0 = *reinterpret_cast<const uint2 *>(v0), s1 = *reinterpret_cast<const uint2 *>(v1);
+          const uint2 s2 = *reinterpret_cast<const uint2 *>(v0 + 64), s3 = *reinterpret_cast<const uint2 *>(v1 + 64);
+          const uint32_t zx = zeros_f16(__byte_perm(vz0.word(t), vz1.word(t), 0x5410)),
+                         zy = zeros_f16(__byte_perm(vz0.word(t), vz1.word(t), 0x7632));
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) {  // four elements: 16 g + 4 q4 .. + 3
+            const uint32_t w0 = q4 < 2 ? s0.x : s0.y, w1 = q4 < 2 ? s1.x : s1.y, w2 = q4 < 2 ? s2.x : s2.y,
+                           w3 = q4 < 2 ? s3.x : s3.y;
+            const uint32_t sel = (q4 & 1) ? 0x7632u : 0x5410u;
+            uint32_t x = __byte_perm(w0, w1, sel), y = __byte_perm(w2, w3, sel);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t a0 = codes_lo(x, zx), a1 = codes_hi(x, zx), a2 = codes_lo(y, zy), a3 = codes_hi(y, zy);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                mma_f16(acc[n][2 * q4 + k], a0, a1, a2, a3, ph[n][2 * t], ph[n][2 * t + 1]);
+                if constexpr (F32) mma_f16(acc[n][2 * q4 + k], a0, a1, a2, a3, pl[n][2 * t], pl[n][2 * t + 1]);
+              }
+              x >>= 8;
+              y >>= 8;
+            }
+          }
+        }
+        __syncwarp();
+        if (i + 1 < end) fetch(1, page1, start_of(i + 1));
+        page0 = page1;
+        page1 = page2;
+        if constexpr (F32) {
+          // the tensor cores truncate each sum, so a long chain is a little too small (1.4e-6 of the
+          // norm over 870 slots): fp32 results take the chain to a rounded sum every few blocks
+          if ((++chain & 3) == 0 || i + 1 == end) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  o[n][t][e] += acc[n][t][e];
+                  acc[n][t][e] = 0.0f;
+                }
+          }
+        }
+      }
+      if constexpr (!F32) {
+        if (more) add_ended();
+        if (i < end) {
+          more = true;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              volatile float *now = ended[2 * n + r];
+#pragma unroll
+              for (int t = 0; t < 8; ++t) {
+                now[2 * t] = o[n][t][r];
+                now[2 * t + 1] = o[n][t][2 + r];
+                o[n][t][r] = o[n][t][2 + r] = 0.0f;
+              }
+              now[16] = l[n][r];
+              now[17] = m[n][r];
+              l[n][r] = 0.0f;
+            }
         }
       }
     }

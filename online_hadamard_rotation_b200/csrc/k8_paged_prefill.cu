@@ -67,6 +67,10 @@ constexpr uint32_t kOffQ = 0, kOffK = 2 * kOperand, kOffV = 4 * kOperand, kOffS 
 constexpr float kRoom = 4.0f;
 constexpr float kRaise = 10.0f;
 constexpr float kCode = 512.0f; // what the codes' 2^-9 takes out
+// Tiles (of eight value products) after which a chain of products ends: the tensor cores truncate as
+// they add, 2^-23 of the sum at most, 2^-15 in a chain. (Without an end 1.3e-3 of the result over 262144
+// slots, 7.2e-3 over 2^20.)
+constexpr int kChain = 32;
 constexpr long long kTimeoutCycles = 4000000000LL;  // about two seconds
 
 struct Shared {
@@ -339,7 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
       tc::mbar_arrive(&S.qfull);
     }
     const bool owns = __any_sync(0xFFFFFFFFu, own != 1.0f);
-    float m = -INFINITY, l = 0.0f;
+    float m = -INFINITY, l = 0.0f, l_ended = 0.0f;
+    float ended[kD];  // the chains that ended; in local memory, touched once a chain
     bool ok = w < halves;
     for (int i = 0; ok && i < tiles; ++i) {
       const int st = i & 1;
@@ -411,11 +416,13 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
       }
       // ---- raise the reference where a weight could exceed it by too much
       const bool raise = top > m + kRoom + kRaise;  // false while both are -inf
-      if (__any_sync(0xFFFFFFFFu, raise)) {
+      const bool chained = i > 0 && i % kChain == 0;  // the chain before ends here
+      if (__any_sync(0xFFFFFFFFu, raise) || chained) {
         const float mn = raise ? top - kRoom : m;
         const float fac = raise ? ex2(m - mn) : 1.0f;
         m = mn;
         l *= fac;
+        l_ended *= fac;
         if (i > 0) {
           // the products of the tile before have been added
           if (!(ok = wait_warp(&S.pvdone[w], (uint32_t)(i - 1) & 1u, S))) break;
@@ -426,10 +433,19 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
             tmem_ld16(o_at + 16u * c, o);
             tc::tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fac);
-            tmem_st16(o_at + 16u * c, o);
+            for (int k = 0; k < 16; ++k) {
+              const float x = __uint_as_float(o[k]) * fac;
+              const float y = i > kChain ? ended[16 * c + k] * fac : 0.0f;
+              o[k] = __float_as_uint(x);
+              if (chained || i > kChain) ended[16 * c + k] = chained ? x + y : y;
+            }
+            if (!chained) tmem_st16(o_at + 16u * c, o);  // else the next product starts from 0
           }
-          tmem_wait_st();
+          if (!chained) tmem_wait_st();
+        }
+        if (chained) {
+          l_ended += l;
+          l = 0.0f;
         }
       }
       // ---- weights over the scores: 64 scores become 32 columns that do not reach past them
@@ -466,6 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
     if (ok && tiles > 0) ok = wait_warp(&S.pvdone[w], (uint32_t)(tiles - 1) & 1u, S);
     if (w < halves && ok) {
       tc::tc_fence_after();
+      l += l_ended;
       const bool none = l == 0.0f;  // no slot seen; a NaN among the scores made l NaN
       const float inv = kCode / l;
 #pragma unroll 1
@@ -474,6 +491,10 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
         if (tiles > 0) {
           tc::tmem_ld32(o_at + 32u * c, x);
           tc::tmem_wait_ld();
+        }
+        if (tiles > kChain) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) + ended[32 * c + k]);
         }
         if (!in) continue;
         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + qrow + 32 * c);
@@ -631,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
         for (int k = 0; k < 8; ++k)  // O_w += P_w V, 16 slots a step
           umma_tmem_a(tmem + 256u + 128u * w, tmem + 128u * w + 8u * k,
                       dv + (uint32_t)st * (kOperand >> 4) + (uint32_t)k * (16u * 128u >> 4), idesc(true),
-                      (i > 0 || k > 0) ? 1u : 0u);
+                      (i % kChain > 0 || k > 0) ? 1u : 0u);
         tc::umma_commit(&S.pvdone[w]);
         if (w == halves - 1) tc::umma_commit(&S.vempty[st]);
         if (i + 1 < tiles) {

@@ -228,3 +228,41 @@ def test_value_scales_far_apart(spin_gpu, shape, small, dtype):
         floor = 32 * floor
     got = run(spin_gpu, q, cache, table, lens, cu, out_dtype=dtype, **kw)
     ref.check_attention(got, (*want[:3], floor, want[4]), "bf16" if dtype == BF16 else "")
+
+
+@pytest.mark.parametrize("most,dtype", [(4096, BF16), (1, BF16), (1, F32), (4, F32)])
+def test_long_sums_are_not_too_small(spin_gpu, most, dtype):
+    """262144 slots of positive values: tensor cores truncate as they add, which a long chain of sums
+    shows as results that are too small on average. Chains of at most 256 products of 2^-23 each, 2^-15
+    together, for bf16 results; of 16 for fp32 ones, 2^-19, whose other errors (sums of at most 2^12
+    rounded terms, 2^-24 each and of either sign; weights of 2^-22) stay below 2^-17 on average. Results
+    differ by several bf16 steps (a row's weight lies on some 1000 slots), so their 8192 roundings of at
+    most 2^-9 are of either sign: their mean is below 2^-13, seven standard deviations of
+    2^-9 / sqrt(3 * 8192) < 2^-16."""
+    n, nq, hq, page = 1 << 18, 4096, 4, 128
+    g = torch.Generator(device="cuda").manual_seed(1)
+    cache = spin_gpu.alloc_kv_cache(n // page, 1, page)
+    for name in ref.CODES:
+        cache[name].copy_(torch.randint(0, 256, cache[name].shape, generator=g, device="cuda", dtype=torch.uint8))
+    cache["k_scale"].fill_(0.5)
+    cache["k_zero"].fill_(7)
+    cache["v_scale"].copy_(0.05 + 0.4 * torch.rand(cache["v_scale"].shape, generator=g, device="cuda"))
+    q = torch.randn((nq, hq, 128), generator=g, device="cuda").bfloat16()
+    table = torch.arange(n // page, dtype=torch.int32, device="cuda")[None].contiguous()
+    got = run(spin_gpu, q, cache, table, [n], [0, nq], max_q_len=most, out_dtype=dtype)
+
+    def rows(name):
+        x = cache[name + "_cache"][:, 0].reshape(n, 64)
+        z, s = (cache[name + e].reshape(n, 1).double() for e in ("_zero", "_scale"))
+        return (torch.stack([x & 15, x >> 4], -1).flatten(1).double() - z) * s
+
+    k, v = rows("k"), rows("v")
+    tokens = torch.arange(0, nq, nq // 16, device="cuda")
+    off = []
+    for h in range(hq):
+        score = q[tokens, h].double() @ k.T / math.sqrt(128)
+        score.masked_fill_(torch.arange(n, device="cuda") > n - nq + tokens[:, None], -math.inf)
+        want = torch.softmax(score, 1) @ v
+        off.append((got[tokens, h].double() - want) / want)
+    mean = float(torch.stack(off).mean())
+    assert abs(mean) < (2 ** -15 + 2 ** -13 if dtype == BF16 else 2 ** -17), mean
