@@ -566,7 +566,8 @@ spin_status_t spin_device_status(uint32_t *status, int reset);
 
 /*
  * Test hook for failure detection (no counterpart on the pages). While
- * enabled (nonzero), every tensor-core R4 launch withholds the completion
+ * enabled (nonzero), every tensor-core R4 launch, and every launch of paged
+ * attention's kernel for chunks of prompts, withholds the completion
  * signal of its first MMA group and shortens its wait budget to about a
  * millisecond, so the bounded waits run out, each block takes its abort path
  * (drains its copies and MMAs, frees TMEM, returns) and the device status word

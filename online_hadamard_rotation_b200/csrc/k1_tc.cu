@@ -1294,6 +1294,7 @@ cudaError_t launch_rotate_quant_tc(int log_n, int bits, const void *x, int64_t t
   return cudaErrorInvalidValue;
 }
 
+int stall_test() { return g_stall_test.load(std::memory_order_relaxed); }
 void set_stall_test(int enable) { g_stall_test.store(enable ? 1 : 0, std::memory_order_relaxed); }
 
 cudaError_t read_device_status(unsigned int *status, bool reset) {

@@ -72,9 +72,11 @@ constexpr float kCode = 512.0f; // what the codes' 2^-9 takes out
 // slots, 7.2e-3 over 2^20.)
 constexpr int kChain = 32;
 constexpr long long kTimeoutCycles = 4000000000LL;  // about two seconds
+constexpr long long kStallTestCycles = 2000000LL;   // about a millisecond, for the stall test hook
 
 struct Shared {
   uint64_t qfull, kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], pvdone[2], drain;
+  long long budget;            // clock cycles a wait may take
   uint32_t tmem_base;
   int abort;
   int seq, pair;               // the block's item
@@ -95,7 +97,7 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Shared &S, 
   while (true) {
     if (tc::mbar_try_wait(bar, parity)) return true;
     if (honor_abort && *reinterpret_cast<volatile int *>(&S.abort)) return false;
-    if (clock64() - t0 > kTimeoutCycles) {
+    if (clock64() - t0 > S.budget) {
       *reinterpret_cast<volatile int *>(&S.abort) = 1;
       atomicOr(&g_prefill_status, 1u);
       return false;
@@ -213,7 +215,7 @@ struct Slot {  // what a converter holds of its slot of a tile
   bool has;  // a page, and a row that may see it
 };
 
-__global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs a, int stall_test) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   Shared &S = *reinterpret_cast<Shared *>(smem + kOffS);
@@ -283,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
     }
     tc::mbar_init(&S.drain, 1);
     S.abort = 0;
+    S.budget = stall_test ? kStallTestCycles : kTimeoutCycles;
     tc::fence_barrier_init();
   }
   if (warp == 12) {
@@ -625,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
     const uint64_t dq = tc::smem_desc(tc::smem_u32(smem + kOffQ), 16, 1024);
     const uint64_t dk = tc::smem_desc(tc::smem_u32(smem + kOffK), 16, 1024);
     const uint64_t dv = tc::smem_desc(tc::smem_u32(smem + kOffV), kTile * 128u, 1024);
-    auto scores = [&](int w, int st) {  // S_w = Q_w K^T
+    auto scores = [&](int w, int st, bool signal = true) {  // S_w = Q_w K^T
       const uint64_t qw = dq + (uint32_t)w * (kOperand >> 4), kw = dk + (uint32_t)st * (kOperand >> 4);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -633,12 +636,12 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
         const uint32_t at = (uint32_t)(k >> 2) * kAtom + (uint32_t)(k & 3) * 2u;
         tc::umma_bf16(tmem + 128u * w, qw + at, kw + at, idesc(false), k > 0 ? 1u : 0u);
       }
-      tc::umma_commit(&S.sfull[w]);
+      if (signal) tc::umma_commit(&S.sfull[w]);
     };
     bool ok = wait(&S.qfull, 0, S) && wait(&S.kfull[0], 0, S);
     if (ok) {
       tc::tc_fence_after();
-      for (int w = 0; w < halves; ++w) scores(w, 0);
+      for (int w = 0; w < halves; ++w) scores(w, 0, !(stall_test && w == 0));
       tc::umma_commit(&S.kempty[0]);
     }
     for (int i = 0; ok && i < tiles; ++i) {
@@ -701,7 +704,7 @@ cudaError_t launch_paged_prefill(const PagedArgs &a, cudaStream_t stream) {
   const int64_t most = rows / (a.row_limit + 1) < a.seqs ? rows / (a.row_limit + 1) : a.seqs;
   const int64_t grid = (rows / kRows + most) * a.hkv;
   if (grid <= 0) return cudaSuccess;
-  k8_paged_prefill<<<(unsigned)grid, kThreads, kSmemBytes, stream>>>(a);
+  k8_paged_prefill<<<(unsigned)grid, kThreads, kSmemBytes, stream>>>(a, stall_test());
   return cudaGetLastError();
 }
 

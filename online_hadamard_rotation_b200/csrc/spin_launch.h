@@ -97,6 +97,7 @@ cudaError_t launch_rotate_quant_tc(int log_n, int bits, const void *x, int64_t t
 
 // Test hook: make the tensor-core R4 kernel withhold one internal signal.
 void set_stall_test(int enable);
+int stall_test();
 
 // Device status words set by kernels whose bounded waits ran out (the tensor-core
 // R4 kernel, the R3 kernel and the tensor-core dequantise kernel each keep one).
