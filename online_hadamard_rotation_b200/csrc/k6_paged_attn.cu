@@ -136,9 +136,9 @@ __device__ __forceinline__ int item_units(const PagedArgs &a, const Blocks &bl) 
 }
 
 template <int R>
-__device__ __forceinline__ int row_tiles(const PagedArgs &a, const Seq &s) {
+__device__ __forceinline__ int row_tiles(const PagedArgs &a, const Seq &s, int limit) {
   const int rows = s.nq * a.group;
-  return rows > a.row_limit ? 0 : (rows + R - 1) / R;
+  return rows > limit ? 0 : (rows + R - 1) / R;
 }
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
@@ -829,8 +829,20 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k6_paged_attn(const
   // ---- the units of all sequences before each thread's share of them
   const int per = (a.seqs + kThreads - 1) / kThreads;
   const int b0 = min(t * per, a.seqs), b1 = min(b0 + per, a.seqs);
+  int limit = a.row_limit;
+  if (limit != INT_MAX) {  // sequences above the limit are the other kernel's, unless there are too few
+    int wide = 0;
+    for (int b = b0; b < b1; ++b) wide += wide_blocks(a, load_seq(a, b));
+    wide = __reduce_add_sync(0xFFFFFFFFu, wide);
+    if (lane == 0) sm.scan[warp] = wide;
+    __syncthreads();
+    long long all = 0;
+    for (int w = 0; w < kWarps; ++w) all += sm.scan[w];
+    if (all * a.hkv < kWideBlocks) limit = INT_MAX;
+    __syncthreads();
+  }
   auto units = [&](const Seq &s, const Blocks &bl) {
-    return (long long)a.hkv * row_tiles<R>(a, s) * item_units(a, bl);
+    return (long long)a.hkv * row_tiles<R>(a, s, limit) * item_units(a, bl);
   };
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
@@ -914,7 +926,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k6_paged_attn(const
         ++b;
         continue;
       }
-      const int tiles = row_tiles<R>(a, s), len = item_units(a, bl);
+      const int tiles = row_tiles<R>(a, s, limit), len = item_units(a, bl);
       const long long item = quot(u - base, len);
       const int off = (int)((u - base) - item * len);
       const int h = (int)quot(item, tiles), rt = (int)(item - (long long)h * tiles);

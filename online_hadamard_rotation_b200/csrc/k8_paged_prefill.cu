@@ -55,7 +55,7 @@ namespace {
 
 constexpr int kD = 128;
 constexpr int kThreads = 13 * 32;
-constexpr int kRows = 256;      // rows of a block of threads, two halves of 128
+constexpr int kRows = kWideRows;  // rows of a block of threads, two halves of 128
 constexpr int kTile = 128;      // slots of a tile
 constexpr uint32_t kOperand = kTile * kD * 2;  // bytes of a 128 x 128 fp16 operand
 constexpr uint32_t kOffQ = 0, kOffK = 2 * kOperand, kOffV = 4 * kOperand, kOffS = 6 * kOperand;
@@ -227,11 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
   {
     const int per = (a.seqs + kThreads - 1) / kThreads;
     const int b0 = min(t * per, a.seqs), b1 = min(b0 + per, a.seqs);
-    auto pairs = [&](int b) {
-      const Seq s = load_seq(a, b);
-      const int rows = s.nq * a.group;
-      return rows > a.row_limit ? (rows + kRows - 1) / kRows : 0;
-    };
+    auto pairs = [&](int b) { return wide_blocks(a, load_seq(a, b)); };
     int mine = 0;
     for (int b = b0; b < b1; ++b) mine += pairs(b);
     int upto = mine;
@@ -243,8 +239,12 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
     if (lane == 31) S.sums[warp] = upto;
     if (t == 0) S.seq = -1;
     __syncthreads();
-    int before = upto - mine;
-    for (int w = 0; w < warp; ++w) before += S.sums[w];
+    int before = upto - mine, all = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += S.sums[w];
+      all += S.sums[w];
+    }
+    if ((int64_t)all * a.hkv < kWideBlocks) return;  // the narrow kernel's
     if (want >= before && want < before + mine)
       for (int b = b0; b < b1; ++b) {
         const int n = pairs(b);
@@ -688,10 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
 }  // namespace
 
 bool paged_prefill_worth(int tokens, int group, int n_kv_heads) {
-  // below a quarter of a block per SM the finer cuts of the narrow kernel fill the GPU better: one
-  // sequence of 2048 slots, 8 kv heads of 4, with 150 new tokens (18 blocks) takes 38.9 us there and
-  // 57.6 here, with 300 (37 blocks) 64.5 and 58.5, with 592 103 and 58
-  return (int64_t)n_kv_heads * tokens * group / kRows >= 37;
+  return (int64_t)n_kv_heads * tokens * group / kRows >= kWideBlocks;
 }
 
 cudaError_t launch_paged_prefill(const PagedArgs &a, cudaStream_t stream) {

@@ -110,8 +110,21 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t *r) {
       : "memory");
 }
 
-// The tcgen05 kernel for sequences with more than row_limit rows (k8_paged_prefill.cu): whether a
-// call of this size has enough of them to fill the GPU, its launch, its status word.
+// Blocks of kWideRows rows that a sequence of more than row_limit rows makes per kv head in the
+// tcgen05 kernel (k8_paged_prefill.cu). A call with fewer than kWideBlocks of them in all leaves them to
+// the narrow kernel, whose finer cuts fill the GPU better: one sequence of 2048 slots, 8 kv heads of 4,
+// with 150 new tokens (24 blocks) takes 38.9 us there and 57.6 in wide blocks, with 300 (40 blocks) 64.5
+// and 58.5, with 592 103 and 58. Only the device knows the sequences' tokens: both kernels count, and
+// one of them leaves. (By the call's tokens alone, 280 single tokens over 2048 slots and one chunk of 20
+// over 32768 took 952 us, the chunk's 8 wide blocks first; 277 so.)
+constexpr int kWideRows = 256;
+constexpr int kWideBlocks = 37;
+__device__ __forceinline__ int wide_blocks(const PagedArgs &a, const Seq &s) {
+  const int rows = s.nq * a.group;
+  return rows > a.row_limit ? (rows + kWideRows - 1) / kWideRows : 0;
+}
+
+// The launch of the tcgen05 kernel, and whether the tokens of a call can make enough blocks for it.
 bool paged_prefill_worth(int tokens, int group, int n_kv_heads);
 cudaError_t launch_paged_prefill(const PagedArgs &a, cudaStream_t stream);
 
