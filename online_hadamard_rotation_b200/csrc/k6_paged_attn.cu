@@ -21,11 +21,12 @@
 //            it (or with a constant in y's place) the terms to cancel can outgrow the result: with
 //            an outlier in a value row most codes sit at the zero; measured 5e-5 of the norm on
 //            65537 slots. A masked slot's stale zero is four bits too, so no NaN enters a product.
-// A query row is scaled by a power of two to a largest value of 2^14 .. 2^15, so its
-// bf16 values are exact in fp16 down to 2^-39 of the largest: the products of the scores are
-// exact. w is one fp16 term (half a step is 2^-12 of it, an eighth of the bf16 result's own
-// rounding; a bf16 term would match that), for fp32 results two (2^-23); its reference is chosen so
-// that it stays below 2^15 whatever the value scales. Sums are fp32.
+// A query row is scaled by a power of two to a largest value of 2^14 .. 2^15 (an odd element's is a
+// sixteenth of that), so its bf16 values are exact in fp16 down to 2^-27 of the largest, and off by
+// 2^-35 of it at most below: the products of the scores are exact but for that. w is one fp16 term (off
+// by 2^-11 of it at most, an eighth of what the bf16 result's own rounding may be; a bf16 term would
+// match that), for fp32 results two (2^-22); its reference is chosen so that it stays below 2^15
+// whatever the value scales. Sums are fp32.
 //
 // The matrices are transposed against the usual form: slots (keys) and head elements
 // (values) are the M side of mma.m16n8k16 and the query rows the N side, so that a decode
@@ -62,18 +63,22 @@
 // cuts from lens and cu_q itself: the host reads nothing back, and no atomics are used, so
 // results repeat bit for bit.
 //
-// What bounds it: instructions. A block of 64 slots and 8 rows costs a warp about 1300 (expanding
-// 8 KB of codes, 64 products, the softmax of 16 numbers a lane); three warps a scheduler issue 0.65 a
-// cycle while they run (0.46 over a launch of 28 us) with the ALU at 40 %. Measured (8 kv heads, 4 query
-// heads each but for the drafts' 8):
-//   32 sequences of up to 4096 slots, one token        28.6 us, 2.6 TB/s (a copy's time: 11.2 us)
-//   4 sequences of 40001 to 65537 slots, fp32 results  61.4 us, 3.4 TB/s (32.1)
-//   16 sequences, four tokens, window 4096, 4 sinks    57.8 us, 1.2 TB/s (10.6); 32 rows a kv head are
+// What bounds it: latency with few warps. A block of 64 slots and 8 rows costs a warp about 1300
+// instructions (expanding 8 KB of codes, 64 products, the softmax of 16 numbers a lane), and the 151
+// registers leave three warps a scheduler, each a chain of copy, scores, softmax and values. They issue
+// in 47 % of the cycles of a launch (at every cycle its instructions would take 10 us); a warp waits 1.2
+// cycles an instruction for the result before it, 0.6 for another warp's turn, 0.6 for memory, 0.5 at
+// the barriers of the start and the join. ALU 40 %, tensor 17 %. Measured (device time; 8 kv heads, 4
+// query heads each but for the drafts' 8):
+//   32 sequences of up to 4096 slots, one token        29.3 us, 2.5 TB/s (a copy's time: 11.2 us)
+//   4 sequences of 40001 to 65537 slots, fp32 results  62.6 us, 3.4 TB/s (32.1)
+//   16 sequences, four tokens, window 4096, 4 sinks    60.7 us, 1.1 TB/s (10.6); 32 rows a kv head are
 //                                                      two tiles, each expands the codes
-//   one sequence of 257 slots                          10 us: the latency of cuts, first loads, softmax
+//   one sequence of 257 slots                          10.5 us: the latency of cuts, first loads, softmax
 //                                                      and join in a row
-// Blocks of threads with 3 instead of 2 to an SM (16-row tiles, 168 registers) take 61.4 us for the
-// drafts.
+// (Times in the reasons for a choice are those of the day it was made, both sides alike.)
+// Blocks of threads with 3 instead of 2 to an SM (16-row tiles, 168 registers) took 61.4 us for the
+// drafts, 57.8 so.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -120,10 +120,12 @@ struct SlotArgs {
 
 // A block finds the rows of its entries once, then its warps take (head, 32 entries) tasks:
 // codes as 16-byte pieces, four lanes a slot, eight loads in flight; steps one slot a lane, so
-// runs of kept slots read and write runs of halves. Memory-bound where many slots move: 8 sequences
-// that keep up to 20011 of 32768 slots (125 MB read and written) take 28 us, 4.5 TB/s (a kept slot is
-// 64-byte code rows and 2-byte steps, half-filled sectors where its neighbour was dropped); 32
-// sequences that keep up to 5 of 8 take 4.3 us.
+// runs of kept slots read and write runs of halves. Where many slots move it waits for memory, with
+// too few bytes in flight to fill it: 8 sequences that keep up to 20011 of 32768 slots (125 MB read and
+// written, 19 us of a copy) take 28 us, 4.5 TB/s. DRAM is at 44 %, a warp waits 24 cycles an instruction
+// for its loads; a block's warps do four tasks one after another, loads before stores. The codes are
+// whole sectors; the 2-byte steps beside dropped ones waste half of theirs at most, 6 % of the bytes. 32
+// sequences that keep up to 5 of 8 take 4.5 us.
 __global__ void __launch_bounds__(kSlotThreads) k7_copy_slots(const SlotArgs a) {
   __shared__ int64_t from[kSlotEntries], to[kSlotEntries];
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -245,7 +247,8 @@ __device__ __forceinline__ int holders(const PoolArgs &a, int64_t row, int64_t c
 // that it did not keep alone are looked at. A decode step wants at most a page or two a row, which its thread
 // looks up and writes itself; the long rows of a prompt are left to whole warps (with warps for
 // every row, 1280 rows took 30 us). The order of rows decides who is served, so one block scans
-// them all; it is bound by the latency of that chain of loads: 1280 rows take 7 us.
+// them all; it is bound by the latency of that chain of loads: 1280 rows take 12 us (7 without the
+// looks at kept and shared pages).
 __global__ void __launch_bounds__(kPlanThreads)
     k7_reserve(const PoolArgs a, const int32_t *__restrict__ add, int32_t *__restrict__ status) {
   __shared__ long long sums[kPlanThreads / 32];
@@ -491,7 +494,7 @@ constexpr int kFreeThreads = 128;
 // Free, first step: block i takes row list[i] (whoever takes its length first), empties its
 // columns and drops its pages, those among them that a cut left behind its length (up to the first
 // column that names none). A page whose last holder left is marked by kFreed. Integer atomics:
-// their order changes no result. 1024 rows take 8 us.
+// their order changes no result. 1024 rows take 6 us.
 __global__ void __launch_bounds__(kFreeThreads) k7_free_rows(const PoolArgs a, const int32_t *__restrict__ list) {
   __shared__ int s_len, s_end;
   tc::grid_dep_launch();

@@ -16,7 +16,8 @@
 // as K-major and MN-major operands with the 128-byte swizzle (eight codes of a word come out in
 // the order 0, 4, 1, 5, 2, 6, 3, 7; the queries are packed alike and the output is put back).
 // Queries are scaled by a power of two, one for the block where its rows allow it (the keys' scales
-// then carry all that a score lacks), so they are exact in fp16.
+// then carry all that a score lacks), so they are exact in fp16 but for elements below 2^-23 of their
+// row's largest, which are off by 2^-31 of it at most.
 //   warps 0-3, 4-7  softmax of rows 0-127 and 128-255: a thread owns a row (a TMEM lane), reads its
 //                   scores, writes the weights p s' as fp16 over them (the A operand of the value
 //                   product stays in TMEM), and rescales its sums only when its reference moves
@@ -28,10 +29,11 @@
 // spin_device_status), stops, waits for its products and frees TMEM.
 //
 // Measured, 3 sequences of up to 4096 slots with 1027 to 2048 new tokens, 32 query and 8 kv heads:
-// 306 us, 637 TFLOP/s (four products' flops per visible slot). No unit is full there: tensor cores
-// and exponentials a third each, ALU 28 %, issue 38 %. No better on the same work: weights as a
-// shared-memory operand with the next scores issued before the value products (311 against 311
-// then), the same with 16 softmax warps of 16 rows (316) and 8 converters (321), scores held in
+// 337 us, 579 TFLOP/s (four products' flops per visible slot). No unit is full there: tensor cores
+// and exponentials 31 % each, ALU 27 %, issue 36 %; one half's chain of scores, softmax and value
+// product has the other half's to hide behind, and no second block on the SM. No better, when the same
+// work took 311 us: weights as a shared-memory operand with the next scores issued before the value
+// products (311), the same with 16 softmax warps of 16 rows (316) and 8 converters (321), scores held in
 // registers between the passes (330 and more). In the widest of these, leaving out the exponentials
 // gained 6 %, seven eighths of the products 11 %, three quarters of the expansion 11 %, half of the
 // second pass over the scores 15 %: the units wait for one another.
@@ -624,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
   } else if (lane == 0 && tiles > 0) {
     // ================================================================ products
     // descriptors of the first step; a step adds its byte offset / 16 to the address field. (One
-    // thread issues 32 products of 32 cycles a tile: what it does between them counts.)
+    // thread issues a tile's 32 products: what it does between them counts.)
     const uint64_t dq = tc::smem_desc(tc::smem_u32(smem + kOffQ), 16, 1024);
     const uint64_t dk = tc::smem_desc(tc::smem_u32(smem + kOffK), 16, 1024);
     const uint64_t dv = tc::smem_desc(tc::smem_u32(smem + kOffV), kTile * 128u, 1024);

@@ -245,8 +245,8 @@ def test_long_sums_are_not_too_small(spin_gpu, most, dtype):
     together, for bf16 results; of 16 for fp32 ones, 2^-19, whose other errors (sums of at most 2^12
     rounded terms, 2^-24 each and of either sign; weights of 2^-22) stay below 2^-17 on average. Results
     differ by several bf16 steps (a row's weight lies on some 1000 slots), so their 8192 roundings of at
-    most 2^-9 are of either sign: their mean is below 2^-13, seven standard deviations of
-    2^-9 / sqrt(3 * 8192) < 2^-16."""
+    most 2^-8 are of either sign: their mean is below 2^-13, four standard deviations of
+    2^-8 / sqrt(3 * 8192) < 2^-15."""
     n, nq, hq, page = 1 << 18, 4096, 4, 128
     g = torch.Generator(device="cuda").manual_seed(1)
     cache = spin_gpu.alloc_kv_cache(n // page, 1, page)
