@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) k8_paged_prefill(const PagedArgs 
       const int E = min(max((int)btop - 128, -40), 60);
       const int er = top == 0u || (e <= E && e >= E - 8) ? E : e;
       const float up = __int_as_float((14 - er + 127) << 23);
-      own = __int_as_float((max(er - E, -126) + 127) << 23);
+      own = __int_as_float((min(max(er - E, -126), 127) + 127) << 23);  // beyond: rows that are not finite
       if (t == 0) S.kmul = __int_as_float((127 + E - 14) << 23) * kCode * a.scale_log2;
       uint8_t *qs = smem + kOffQ + w * kOperand;
 #pragma unroll 4

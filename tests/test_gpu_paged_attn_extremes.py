@@ -274,3 +274,22 @@ def test_long_sums_are_not_too_small(spin_gpu, most, dtype):
         off.append((got[tokens, h].double() - want) / want)
     mean = float(torch.stack(off).mean())
     assert abs(mean) < (2 ** -15 + 2 ** -13 if dtype == BF16 else 2 ** -17), mean
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", ["drafts", "chunk"])
+def test_infinite_queries_among_tiny_ones(spin_gpu, shape, dtype):
+    """An infinite query whose scores are all +inf gives NaN, whatever the sizes of the rows beside it."""
+    lens, nq, q, cache, table, cu, kw, _, _ = some(shape, 13)
+    for name in ("k_cache", "k_zero"):
+        cache[name].fill_(0 if name == "k_zero" else 0x33)
+    q *= 2.0 ** -50
+    q[nq[0] // 2] = 1
+    q[nq[0] // 2, :, 7] = math.inf
+    got = run(spin_gpu, q, cache, table, lens, cu, out_dtype=dtype, **kw)
+    rows = torch.ones(q.shape[0], dtype=torch.bool)
+    rows[nq[0] // 2] = False
+    assert torch.isnan(got[~rows]).all() and torch.isfinite(got[rows]).all()
+    q[nq[0] // 2] = 0
+    want = ref.attention(q, cache, table, lens, cu, **kw)
+    check_unseen(got, want, ~rows, "bf16" if dtype == BF16 else "")
